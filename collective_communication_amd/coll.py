@@ -33,6 +33,7 @@ _REDUCE_DTYPES = {torch.bfloat16: COLL_BF16, torch.float16: COLL_FP16,
 
 # exported symbol -> (restype, argtypes)
 _vp, _sz, _i = ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int
+_l, _f = ctypes.c_int64, ctypes.c_float
 SIGNATURES = {
     "coll_status_string": (ctypes.c_char_p, [_i]),
     "coll_version": (_i, []),
@@ -71,6 +72,19 @@ SIGNATURES = {
     "coll_moe_dispatch": (_i, [_i, _vp, _vp, _vp, _vp, _vp, _i, _i, _sz, _i, _vp, _vp, _vp]),
     "coll_moe_combine_recv": (_i, [_i, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _sz, _i, _vp,
                                    _vp, _vp]),
+    "coll_attn_prompt": (_i, [_i, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _l, _l, _i, _i, _i,
+                              _l, _l, _l, _l, _i, _f, _i, _vp]),
+    "coll_attn_decode_workspace_bytes": (_sz, [_i, _i, _l, _i, _i, _i]),
+    "coll_attn_decode": (_i, [_i, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _l, _i, _i,
+                              _i, _i, _l, _l, _l, _l, _l, _f, _i, _vp, _sz, _vp]),
+    "coll_kv_write": (_i, [_i, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _l, _i, _i, _i, _l, _i, _i,
+                           _i, _l, _l, _l, _l, _l, _i, _vp]),
+    "coll_kv_extend": (_i, [_vp, _vp, _vp, _i, _i, _i, _i, _vp, _vp, _i, _vp, _vp]),
+    "coll_kv_fork": (_i, [_vp, _vp, _vp, _i, _i, _i, _i, _vp, _vp, _i, _vp, _vp, _vp, _vp]),
+    "coll_kv_free": (_i, [_vp, _vp, _vp, _i, _i, _i, _vp, _i, _vp]),
+    "coll_kv_compact_workspace_bytes": (_sz, [_i]),
+    "coll_kv_compact": (_i, [_vp, _vp, _i, _i, _i, _vp, _i, _vp, _vp, _sz, _vp]),
+    "coll_kv_copy_pages": (_i, [_i, _vp, _sz, _sz, _sz, _vp, _i, _vp, _vp]),
 }
 
 
@@ -756,3 +770,287 @@ def moe_combine_recv(recvs, pos, sendcounts, sdispls, rdispls, weights, outs, to
                   _table(pos, "pos", R), _dev(sendcounts, "sc"), _dev(sdispls, "sd"),
                   _dev(rdispls, "rd"), _table(weights, "w", R), ids, T, K, H, COLL_BF16,
                   _table(outs, "out", R), _rows(recvs, H))
+
+
+# ------------------------------------------------- attention and its cache
+
+_ATTN_DTYPES = {torch.bfloat16: COLL_BF16, torch.float16: COLL_FP16}
+KV_MAX_ENTRIES = 1024           # COLL_KV_MAX_ENTRIES of include/coll.h
+
+
+def _here(ts, what):
+    """The tensors are on the current device, whose stream the call uses."""
+    for t in ts:
+        if not t.is_cuda or t.get_device() != torch.cuda.current_device():
+            raise ValueError(f"{what}: tensors must be on the current GPU")
+
+
+def _ptrs(ts, what, R):
+    if len(ts) != R:
+        raise ValueError(f"{what}: {len(ts)} buffers for {R} ranks (one per rank)")
+    _here(ts, what)
+    return (ctypes.c_void_p * R)(*[t.data_ptr() for t in ts])
+
+
+def _ints(ts, shape, what, R):
+    """R contiguous int32 tensors of one shape."""
+    for t in ts:
+        if t.dtype != torch.int32 or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+            raise ValueError(f"{what} must be contiguous int32 {list(shape)} on every rank")
+    return _ptrs(ts, what, R)
+
+
+def _heads_rows(ts, shape, dtype, what, R):
+    """R tensors [tokens, heads, head_dim] whose heads are contiguous within a
+    token; returns (pointers, elements between tokens).  The tokens may be
+    apart (a slice of a fused projection), alike on every rank."""
+    stride = None
+    for t in ts:
+        if tuple(t.shape) != tuple(shape) or t.dtype != dtype:
+            raise ValueError(f"{what} must be {list(shape)} of {dtype} on every rank")
+        T, H, D = shape
+        if (D > 1 and t.stride(2) != 1) or (H > 1 and t.stride(1) != D):
+            raise ValueError(f"{what}: the heads of a token must be contiguous")
+        s = t.stride(0) if T > 1 else -(-H * D // 8) * 8
+        if stride is not None and s != stride:
+            raise ValueError(f"{what}: every rank needs the same strides")
+        stride = s
+    return _ptrs(ts, what, R), stride
+
+
+def _pool_tables(ks, vs, dtype, what, R):
+    """The K and V pools [num_pages, page_size, kv_heads, head_dim], strided
+    alike on every rank; returns (k pointers, v pointers, shape, strides)."""
+    shape = tuple(ks[0].shape) if ks else ()
+    if len(shape) != 4:
+        raise ValueError(f"{what}: pools are [num_pages, page_size, kv_heads, head_dim]")
+    strides = None
+    for t in list(ks) + list(vs):
+        if tuple(t.shape) != shape or t.dtype != dtype:
+            raise ValueError(f"{what}: every pool must be {list(shape)} of {dtype}")
+        if shape[3] > 1 and t.stride(3) != 1:
+            raise ValueError(f"{what}: the elements of a head must be contiguous")
+        s = tuple(t.stride(i) if shape[i] > 1 else 0 for i in range(3))
+        if strides is not None and s != strides:
+            raise ValueError(f"{what}: every pool needs the same strides")
+        strides = s
+    return _ptrs(ks, "k pool", R), _ptrs(vs, "v pool", R), shape, strides
+
+
+def _lse_table(lses, rows, heads, what, R):
+    if lses is None:
+        return None
+    for t in lses:
+        if t.dtype != torch.float32 or tuple(t.shape) != (rows, heads) or not t.is_contiguous():
+            raise ValueError(f"{what}: lse must be contiguous fp32 [{rows}, {heads}] on every rank")
+    return _ptrs(lses, "lse", R)
+
+
+def _attn_dtype(t, what):
+    if t.dtype not in _ATTN_DTYPES:
+        raise ValueError(f"{what}: bf16 or fp16, got {t.dtype}")
+    return _ATTN_DTYPES[t.dtype]
+
+
+def attn_prompt(qs, ks, vs, outs, q_starts, k_starts, lses=None, diags=None, causal: bool = True,
+                scale: float | None = None, stream=None):
+    """Attention over packed prompts, one rank per list entry.
+
+    qs[r], outs[r]: [Tq, heads, D]; ks[r], vs[r]: [Tk, kv_heads, D] (bf16 or
+    fp16; tokens may be strided, heads of a token contiguous).  Sequence b has
+    the query rows q_starts[r][b] .. q_starts[r][b+1] and the key rows
+    k_starts[r][b] .. k_starts[r][b+1] (int32 [nseq + 1] on the device).  With
+    ``causal``, its query i sees key j <= i + diag, diag = diags[r][b] (int32
+    [nseq]) or, without ``diags``, keys - queries.  lses[r]: fp32 [Tq, heads],
+    the log-sum-exps that lse_merge takes.  ``scale`` defaults to 1/sqrt(D).
+    A row that sees no key gets 0 and -inf; rows of no sequence are not
+    written."""
+    R = _ranks(qs, "attn_prompt")
+    dt = _attn_dtype(qs[0], "attn_prompt")
+    if qs[0].dim() != 3 or not ks or ks[0].dim() != 3:
+        raise ValueError("attn_prompt: q and k are [tokens, heads, head_dim]")
+    Tq, H, D = qs[0].shape
+    Tk, KV = ks[0].shape[:2]
+    if KV < 1 or H % KV:
+        raise ValueError(f"attn_prompt: {H} heads over {KV} kv heads")
+    q, q_stride = _heads_rows(qs, (Tq, H, D), qs[0].dtype, "q", R)
+    k, k_stride = _heads_rows(ks, (Tk, KV, D), qs[0].dtype, "k", R)
+    v, v_stride = _heads_rows(vs, (Tk, KV, D), qs[0].dtype, "v", R)
+    o, o_stride = _heads_rows(outs, (Tq, H, D), qs[0].dtype, "out", R)
+    n = q_starts[0].numel() - 1
+    if n < 0:
+        raise ValueError("attn_prompt: starts have one entry more than there are sequences")
+    qst, kst = _ints(q_starts, (n + 1,), "q_starts", R), _ints(k_starts, (n + 1,), "k_starts", R)
+    dg = None if diags is None else _ints(diags, (n,), "diags", R)
+    return _issue("coll_attn_prompt", "attn_prompt", stream, R, q, k, v, o,
+                  _lse_table(lses, Tq, H, "attn_prompt", R), qst, kst, dg, n, Tq, Tk, H, KV, D,
+                  q_stride, k_stride, v_stride, o_stride, int(bool(causal)),
+                  D ** -0.5 if scale is None else float(scale), dt)
+
+
+def attn_decode_workspace_bytes(R: int, batch: int, max_len: int, heads: int, kv_heads: int,
+                                head_dim: int) -> int:
+    """Workspace bytes of attn_decode; ``max_len`` is the table's width times
+    the page size."""
+    return int(lib().coll_attn_decode_workspace_bytes(R, batch, max_len, heads, kv_heads, head_dim))
+
+
+def attn_decode(qs, k_pools, v_pools, tables, lens, outs, workspace, lses=None, seqs=None,
+                scale: float | None = None, stream=None):
+    """Attention of one new token over a paged cache, one rank per list entry.
+
+    qs[r], outs[r]: [batch, heads, D]; k_pools[r], v_pools[r]: [num_pages,
+    page_size, kv_heads, D] views (any order of the first three axes in
+    memory); tables[r]: int32 [rows, max_pages] page ids; lens[r]: int32
+    [rows] tokens in the cache.  Entry b reads row b, or row seqs[r][b] (int32
+    [batch]).  lses[r]: fp32 [batch, heads].  ``workspace``: a uint8 tensor of
+    attn_decode_workspace_bytes(R, batch, max_pages * page_size, heads,
+    kv_heads, D) bytes.  An entry with no tokens gets 0 and -inf."""
+    R = _ranks(qs, "attn_decode")
+    dt = _attn_dtype(qs[0], "attn_decode")
+    if qs[0].dim() != 3:
+        raise ValueError("attn_decode: q is [batch, heads, head_dim]")
+    B, H, D = qs[0].shape
+    q, q_stride = _heads_rows(qs, (B, H, D), qs[0].dtype, "q", R)
+    o, o_stride = _heads_rows(outs, (B, H, D), qs[0].dtype, "out", R)
+    kp, vp, (N, P, KV, Dp), strides = _pool_tables(k_pools, v_pools, qs[0].dtype, "attn_decode", R)
+    if Dp != D or KV < 1 or H % KV:
+        raise ValueError(f"attn_decode: {H} heads of {D} over {KV} kv heads of {Dp}")
+    tab, ln, rows, width, sq = _rows_of_cache(tables, lens, seqs, B, "attn_decode", R)
+    _here([workspace], "workspace")
+    return _issue("coll_attn_decode", "attn_decode", stream, R, q, kp, vp, tab, ln, sq, o,
+                  _lse_table(lses, B, H, "attn_decode", R), B, rows, width, N, P, H, KV, D,
+                  q_stride, o_stride, *strides, D ** -0.5 if scale is None else float(scale), dt,
+                  _dev(workspace, "workspace"), workspace.numel() * workspace.element_size())
+
+
+def _rows_of_cache(tables, lens, seqs, batch, what, R):
+    if tables[0].dim() != 2:
+        raise ValueError(f"{what}: tables are int32 [rows, max_pages]")
+    rows, width = tables[0].shape
+    tab, ln = _ints(tables, (rows, width), "tables", R), _ints(lens, (rows,), "lens", R)
+    if seqs is None and batch > rows:
+        raise ValueError(f"{what}: {batch} entries but {rows} table rows (pass seqs)")
+    sq = None if seqs is None else _ints(seqs, (batch,), "seqs", R)
+    return tab, ln, rows, width, sq
+
+
+def kv_write(ks, vs, k_pools, v_pools, tables, lens, starts, seqs=None, stream=None):
+    """Write packed new tokens into the cache: rows starts[r][b] ..
+    starts[r][b+1] of ks[r] and vs[r] ([T, kv_heads, D]) become the last
+    tokens of row b of the table, or of row seqs[r][b] (lens count them
+    already: kv_extend first).  Pools, tables and lens as in attn_decode."""
+    R = _ranks(ks, "kv_write")
+    dt = _attn_dtype(ks[0], "kv_write")
+    if ks[0].dim() != 3:
+        raise ValueError("kv_write: k is [tokens, kv_heads, head_dim]")
+    T, KV, D = ks[0].shape
+    k, k_stride = _heads_rows(ks, (T, KV, D), ks[0].dtype, "k", R)
+    v, v_stride = _heads_rows(vs, (T, KV, D), ks[0].dtype, "v", R)
+    kp, vp, (N, P, KVp, Dp), strides = _pool_tables(k_pools, v_pools, ks[0].dtype, "kv_write", R)
+    if (KVp, Dp) != (KV, D):
+        raise ValueError("kv_write: the pools' heads differ from the tokens'")
+    B = starts[0].numel() - 1
+    if B < 0:
+        raise ValueError("kv_write: starts have one entry more than there are sequences")
+    st = _ints(starts, (B + 1,), "starts", R)
+    tab, ln, rows, width, sq = _rows_of_cache(tables, lens, seqs, B, "kv_write", R)
+    return _issue("coll_kv_write", "kv_write", stream, R, k, v, kp, vp, tab, ln, st, sq, T, B, rows,
+                  width, N, P, KV, D, k_stride, v_stride, *strides, dt)
+
+
+def _kv_state(table, lens, ref, what):
+    """(table, lens, ref pointers, rows, width, pages) of a page state."""
+    if table.dim() != 2 or ref.dim() != 1:
+        raise ValueError(f"{what}: table is int32 [rows, max_pages], ref int32 [num_pages]")
+    rows, width = table.shape
+    ptrs = [_ints([table], (rows, width), "table", 1)[0]]
+    if lens is not None:
+        ptrs.append(_ints([lens], (rows,), "lens", 1)[0])
+    ptrs.append(_ints([ref], tuple(ref.shape), "ref", 1)[0])
+    return (*ptrs, rows, width, ref.numel())
+
+
+def _kv_list(ts, what):
+    """Pointers of int32 [n] lists, and n (at most KV_MAX_ENTRIES)."""
+    n = ts[0].numel()
+    if n > KV_MAX_ENTRIES:
+        raise ValueError(f"{what}: {n} entries (at most {KV_MAX_ENTRIES} a call)")
+    return [_ints([t], (n,), f"{what}: lists", 1)[0] for t in ts], n
+
+
+def _kv_moves(moves, count, most, what):
+    if moves.dtype != torch.int32 or moves.dim() != 2 or moves.shape[1] != 2 or \
+            moves.shape[0] < most or not moves.is_contiguous():
+        raise ValueError(f"{what}: moves must be contiguous int32 [at least {most}, 2]")
+    _here([moves], what)
+    return moves.data_ptr(), _ints([count], (1,), f"{what}: count", 1)[0]
+
+
+def kv_extend(table, lens, ref, seqs, add, page_size: int, status, stream=None):
+    """Grow sequences of the cache: lens[seqs[i]] += add[i], with the lowest
+    free pages for what does not fit the last one.  status[i]: 0, -1 (not
+    valid) or -2 (too few pages); all int32 on the device."""
+    t, l, r, rows, width, pages = _kv_state(table, lens, ref, "kv_extend")
+    (sq, ad, st), n = _kv_list((seqs, add, status), "kv_extend")
+    return _issue("coll_kv_extend", "kv_extend", stream, t, l, r, rows, width, pages, page_size, sq,
+                  ad, n, st)
+
+
+def kv_fork(table, lens, ref, src, dst, page_size: int, moves, count, status, stream=None):
+    """Make the empty rows dst[i] copies of rows src[i]: full pages are shared,
+    a partly filled last page gets a fresh one and an entry in moves (int32
+    [n, 2], *count of them) for kv_copy_pages.  status as in kv_extend."""
+    t, l, r, rows, width, pages = _kv_state(table, lens, ref, "kv_fork")
+    (sr, ds, st), n = _kv_list((src, dst, status), "kv_fork")
+    mv, ct = _kv_moves(moves, count, n, "kv_fork")
+    return _issue("coll_kv_fork", "kv_fork", stream, t, l, r, rows, width, pages, page_size, sr, ds,
+                  n, mv, ct, st)
+
+
+def kv_free(table, lens, ref, seqs, stream=None):
+    """Release the pages of rows seqs[i]; the rows become empty."""
+    t, l, r, rows, width, pages = _kv_state(table, lens, ref, "kv_free")
+    (sq,), n = _kv_list((seqs,), "kv_free")
+    return _issue("coll_kv_free", "kv_free", stream, t, l, r, rows, width, pages, sq, n)
+
+
+def kv_compact_workspace_bytes(num_pages: int) -> int:
+    """Workspace bytes of kv_compact."""
+    return int(lib().coll_kv_compact_workspace_bytes(num_pages))
+
+
+def kv_compact(table, ref, moves, count, workspace, stream=None):
+    """Renumber the pages in use to 0 .. c - 1 (table and ref are rewritten) and
+    list the copies in moves (int32 [at least num_pages / 2, 2], *count of
+    them) for kv_copy_pages on every pool."""
+    t, r, rows, width, pages = _kv_state(table, None, ref, "kv_compact")
+    mv, ct = _kv_moves(moves, count, pages // 2, "kv_compact")
+    _here([workspace], "workspace")
+    return _issue("coll_kv_compact", "kv_compact", stream, t, r, rows, width, pages, mv,
+                  moves.shape[0], ct, _dev(workspace, "workspace"),
+                  workspace.numel() * workspace.element_size())
+
+
+def kv_copy_pages(pools, moves, count=None, layered: bool = False, stream=None):
+    """Copy page moves[m, 0] over page moves[m, 1] in every pool, for m <
+    count (a device int32 [1]) or all of moves (pairs with an index outside
+    the pool are skipped).  pools: up to 16 contiguous tensors [num_pages,
+    ...], or with ``layered`` [layers, num_pages, ...], all of one shape."""
+    n = _ranks(pools, "kv_copy_pages")
+    shape, es = tuple(pools[0].shape), pools[0].element_size()
+    if len(shape) < (3 if layered else 2):
+        raise ValueError("kv_copy_pages: pools are [num_pages, ...] or [layers, num_pages, ...]")
+    for p in pools:
+        if tuple(p.shape) != shape or p.dtype != pools[0].dtype:
+            raise ValueError("kv_copy_pages: every pool needs the same shape and dtype")
+    _here(pools, "kv_copy_pages")
+    layers, pages = (shape[0], shape[1]) if layered else (1, shape[0])
+    if moves.dtype != torch.int32 or moves.dim() != 2 or moves.shape[1] != 2 or \
+            not moves.is_contiguous():
+        raise ValueError("kv_copy_pages: moves must be contiguous int32 [m, 2]")
+    _here([moves], "moves")
+    ct = None if count is None else _ints([count], (1,), "count", 1)[0]
+    each = pools[0].numel() // (layers * pages) * es if layers * pages > 0 else 0
+    return _issue("coll_kv_copy_pages", "kv_copy_pages", stream, n, _table(pools, "pool", n), layers,
+                  pages, each, moves.data_ptr(), moves.shape[0], ct)

@@ -679,4 +679,238 @@ int coll_moe_combine_recv(int R, const void *const *recvbufs, const int32_t *con
                                  topk_ids ? &is : nullptr, tokens, topk, hidden, os, rows);
 }
 
+// ---------------------------------------------- attention and its cache
+
+// dtype, head layout and scale that both attention calls share.
+static int attn_check(int R, int heads, int kv_heads, int head_dim, float scale, int dtype) {
+  if (!ranks_ok(R) || !dtype_ok(dtype) || heads < 1 || kv_heads < 1 || heads % kv_heads != 0 ||
+      heads > (1 << 16) || head_dim < 1)
+    return COLL_ERR_INVALID_ARG;
+  if (scale == 0.0f || scale - scale != 0.0f) return COLL_ERR_INVALID_ARG;
+  if (dtype != COLL_BF16 && dtype != COLL_FP16) return COLL_ERR_UNSUPPORTED;
+  if (head_dim != 64 && head_dim != 96 && head_dim != 128 && head_dim != 192 && head_dim != 256)
+    return COLL_ERR_UNSUPPORTED;
+  return COLL_OK;
+}
+
+// Rows of 16-byte units: `stride` elements of 2 bytes apart, `width` long.
+static bool rows_ok(int64_t rows, int64_t stride, int64_t width) {
+  return stride >= width && stride % 8 == 0 &&
+         (rows == 0 || stride <= ((int64_t)1 << 54) / rows);
+}
+
+static bool all_aligned16(int R, const void *const *p) {
+  for (int r = 0; r < R; r++)
+    if (!aligned16(p[r])) return false;
+  return true;
+}
+
+// Strides of a pool [num_pages][page_size][kv_heads][head_dim] in any order of
+// the first three axes.
+static bool pool_ok(int64_t num_pages, int page_size, int kv_heads, int64_t page_stride,
+                    int64_t tok_stride, int64_t head_stride) {
+  const int64_t lim = (int64_t)1 << 52;
+  if (num_pages < 0 || num_pages > INT32_MAX || page_size < 1) return false;
+  if (page_stride < 0 || tok_stride < 0 || head_stride < 0) return false;
+  if (page_stride % 8 || tok_stride % 8 || head_stride % 8) return false;
+  return page_stride <= lim / (num_pages + 1) && tok_stride <= lim / page_size &&
+         head_stride <= lim / kv_heads;
+}
+
+int coll_attn_prompt(int R, const void *const *q, const void *const *k, const void *const *v,
+                     void *const *o, float *const *lse, const int32_t *const *q_starts,
+                     const int32_t *const *k_starts, const int32_t *const *diag, int nseq,
+                     int64_t q_rows, int64_t k_rows, int heads, int kv_heads, int head_dim,
+                     int64_t q_stride, int64_t k_stride, int64_t v_stride, int64_t o_stride,
+                     int causal, float scale, coll_dtype_t dtype, void *stream) {
+  const int st = attn_check(R, heads, kv_heads, head_dim, scale, dtype);
+  if (st != COLL_OK) return st;
+  if (nseq < 0 || q_rows < 0 || k_rows < 0 || q_rows >= ((int64_t)1 << 31) ||
+      k_rows >= ((int64_t)1 << 31))
+    return COLL_ERR_INVALID_ARG;
+  if (nseq == 0 || q_rows == 0) return COLL_OK;
+  const int64_t qw = (int64_t)heads * head_dim, kw = (int64_t)kv_heads * head_dim;
+  if (!rows_ok(q_rows, q_stride, qw) || !rows_ok(q_rows, o_stride, qw) ||
+      !rows_ok(k_rows, k_stride, kw) || !rows_ok(k_rows, v_stride, kw))
+    return COLL_ERR_INVALID_ARG;
+  PtrTable qt{}, kt{}, vt{}, qs{}, ks{}, dg{};
+  MutPtrTable ot{}, lt{};
+  if (!fill_in(R, q, qt.p) || !fill_out(R, o, ot.p) ||
+      !fill_in(R, reinterpret_cast<const void *const *>(q_starts), qs.p) ||
+      !fill_in(R, reinterpret_cast<const void *const *>(k_starts), ks.p))
+    return COLL_ERR_INVALID_ARG;
+  if (k_rows > 0 && (!fill_in(R, k, kt.p) || !fill_in(R, v, vt.p))) return COLL_ERR_INVALID_ARG;
+  if (diag && !fill_in(R, reinterpret_cast<const void *const *>(diag), dg.p))
+    return COLL_ERR_INVALID_ARG;
+  if (!all_aligned16(R, qt.p) || !all_aligned16(R, kt.p) || !all_aligned16(R, vt.p) ||
+      !all_aligned16(R, const_cast<const void *const *>(ot.p)))
+    return COLL_ERR_INVALID_ARG;
+  if (lse)
+    for (int r = 0; r < R; r++) lt.p[r] = lse[r];            // NULL entries: not written
+  return launch_attn_prompt(launch_ctx(stream), R, qt, kt, vt, ot, lt, qs, ks, dg, nseq, q_rows,
+                            k_rows, heads, kv_heads, head_dim, q_stride, k_stride, v_stride,
+                            o_stride, causal != 0, scale, dtype);
+}
+
+size_t coll_attn_decode_workspace_bytes(int R, int batch, int64_t max_len, int heads, int kv_heads,
+                                        int head_dim) {
+  if (attn_check(R, heads, kv_heads, head_dim, 1.0f, COLL_BF16) != COLL_OK) return 0;
+  if (batch < 1 || max_len < 0 || max_len >= ((int64_t)1 << 31)) return 0;
+  return attn_decode_workspace_bytes(R, batch, max_len, heads, kv_heads, head_dim);
+}
+
+int coll_attn_decode(int R, const void *const *q, const void *const *k_pools,
+                     const void *const *v_pools, const int32_t *const *tables,
+                     const int32_t *const *lens, const int32_t *const *seqs, void *const *o,
+                     float *const *lse, int batch, int table_rows, int max_pages,
+                     int64_t num_pages, int page_size, int heads, int kv_heads, int head_dim,
+                     int64_t q_stride, int64_t o_stride, int64_t page_stride, int64_t tok_stride,
+                     int64_t head_stride, float scale, coll_dtype_t dtype, void *workspace,
+                     size_t workspace_bytes, void *stream) {
+  const int st = attn_check(R, heads, kv_heads, head_dim, scale, dtype);
+  if (st != COLL_OK) return st;
+  if (batch < 0 || batch > (1 << 24) || table_rows < 0 || max_pages < 0 ||
+      !pool_ok(num_pages, page_size, kv_heads, page_stride, tok_stride, head_stride))
+    return COLL_ERR_INVALID_ARG;
+  if (batch == 0) return COLL_OK;
+  if (!seqs && batch > table_rows) return COLL_ERR_INVALID_ARG;
+  const int64_t qw = (int64_t)heads * head_dim;
+  if (!rows_ok(batch, q_stride, qw) || !rows_ok(batch, o_stride, qw)) return COLL_ERR_INVALID_ARG;
+  const int64_t max_len = (int64_t)max_pages * page_size;
+  if (max_len >= ((int64_t)1 << 31)) return COLL_ERR_UNSUPPORTED;
+  PtrTable qt{}, kt{}, vt{}, tt{}, nt{}, sq{};
+  MutPtrTable ot{}, lt{};
+  if (!fill_in(R, q, qt.p) || !fill_out(R, o, ot.p) ||
+      !fill_in(R, reinterpret_cast<const void *const *>(lens), nt.p))
+    return COLL_ERR_INVALID_ARG;
+  if (num_pages > 0 && max_len > 0 && table_rows > 0 &&
+      (!fill_in(R, k_pools, kt.p) || !fill_in(R, v_pools, vt.p) ||
+       !fill_in(R, reinterpret_cast<const void *const *>(tables), tt.p)))
+    return COLL_ERR_INVALID_ARG;
+  if (seqs && !fill_in(R, reinterpret_cast<const void *const *>(seqs), sq.p))
+    return COLL_ERR_INVALID_ARG;
+  if (!all_aligned16(R, qt.p) || !all_aligned16(R, kt.p) || !all_aligned16(R, vt.p) ||
+      !all_aligned16(R, const_cast<const void *const *>(ot.p)))
+    return COLL_ERR_INVALID_ARG;
+  if (lse)
+    for (int r = 0; r < R; r++) lt.p[r] = lse[r];            // NULL entries: not written
+  const size_t need = attn_decode_workspace_bytes(R, batch, max_len, heads, kv_heads, head_dim);
+  if (!workspace || ((uintptr_t)workspace & 255) != 0 || workspace_bytes < need)
+    return COLL_ERR_INVALID_ARG;
+  return launch_attn_decode(launch_ctx(stream), R, qt, kt, vt, tt, nt, sq, ot, lt, batch,
+                            table_rows, max_pages, num_pages, page_size, heads, kv_heads, head_dim,
+                            q_stride, o_stride, page_stride, tok_stride, head_stride, scale, dtype,
+                            workspace);
+}
+
+int coll_kv_write(int R, const void *const *k, const void *const *v, void *const *k_pools,
+                  void *const *v_pools, const int32_t *const *tables, const int32_t *const *lens,
+                  const int32_t *const *starts, const int32_t *const *seqs, int64_t tokens,
+                  int batch, int table_rows, int max_pages, int64_t num_pages, int page_size,
+                  int kv_heads, int head_dim, int64_t k_stride, int64_t v_stride,
+                  int64_t page_stride, int64_t tok_stride, int64_t head_stride,
+                  coll_dtype_t dtype, void *stream) {
+  if (!ranks_ok(R) || !dtype_ok(dtype) || kv_heads < 1 || kv_heads > (1 << 16) || head_dim < 1 ||
+      tokens < 0 || batch < 0 || batch > (1 << 24) || table_rows < 0 || max_pages < 0 ||
+      !pool_ok(num_pages, page_size, kv_heads, page_stride, tok_stride, head_stride))
+    return COLL_ERR_INVALID_ARG;
+  if (dtype_size(dtype) != 2 || head_dim % 8 != 0 || head_dim > 1024) return COLL_ERR_UNSUPPORTED;
+  if (tokens == 0 || batch == 0 || table_rows == 0 || max_pages == 0 || num_pages == 0)
+    return COLL_OK;
+  if (!seqs && batch > table_rows) return COLL_ERR_INVALID_ARG;
+  const int64_t kw = (int64_t)kv_heads * head_dim;
+  if (!rows_ok(tokens, k_stride, kw) || !rows_ok(tokens, v_stride, kw)) return COLL_ERR_INVALID_ARG;
+  if ((int64_t)max_pages * page_size >= ((int64_t)1 << 31) || tokens >= ((int64_t)1 << 31))
+    return COLL_ERR_UNSUPPORTED;
+  PtrTable kt{}, vt{}, tt{}, nt{}, ss{}, sq{};
+  MutPtrTable kp{}, vp{};
+  if (!fill_in(R, k, kt.p) || !fill_in(R, v, vt.p) || !fill_out(R, k_pools, kp.p) ||
+      !fill_out(R, v_pools, vp.p) || !fill_in(R, reinterpret_cast<const void *const *>(tables), tt.p) ||
+      !fill_in(R, reinterpret_cast<const void *const *>(lens), nt.p) ||
+      !fill_in(R, reinterpret_cast<const void *const *>(starts), ss.p))
+    return COLL_ERR_INVALID_ARG;
+  if (seqs && !fill_in(R, reinterpret_cast<const void *const *>(seqs), sq.p))
+    return COLL_ERR_INVALID_ARG;
+  if (!all_aligned16(R, kt.p) || !all_aligned16(R, vt.p) ||
+      !all_aligned16(R, const_cast<const void *const *>(kp.p)) ||
+      !all_aligned16(R, const_cast<const void *const *>(vp.p)))
+    return COLL_ERR_INVALID_ARG;
+  return launch_kv_write(launch_ctx(stream), R, kt, vt, kp, vp, tt, nt, ss, sq, tokens, batch,
+                         table_rows, max_pages, num_pages, page_size, kv_heads, head_dim, k_stride,
+                         v_stride, page_stride, tok_stride, head_stride);
+}
+
+// The arguments all bookkeeping calls share.
+static bool kv_ok(int rows, int max_pages, int num_pages, int page_size) {
+  return rows >= 0 && max_pages >= 0 && num_pages >= 0 && num_pages <= INT32_MAX - 8192 &&
+         page_size >= 1 && ((int64_t)max_pages + 1) * page_size < ((int64_t)1 << 31);
+}
+
+int coll_kv_extend(int32_t *table, int32_t *lens, int32_t *ref, int table_rows, int max_pages,
+                   int num_pages, int page_size, const int32_t *seqs, const int32_t *add, int n,
+                   int32_t *status, void *stream) {
+  if (!kv_ok(table_rows, max_pages, num_pages, page_size) || n < 0 || n > kKvMaxEntries)
+    return COLL_ERR_INVALID_ARG;
+  if (n == 0) return COLL_OK;
+  if (!table || !lens || !ref || !seqs || !add || !status) return COLL_ERR_INVALID_ARG;
+  return launch_kv_extend(launch_ctx(stream), table, lens, ref, table_rows, max_pages, num_pages,
+                          page_size, seqs, add, n, status);
+}
+
+int coll_kv_fork(int32_t *table, int32_t *lens, int32_t *ref, int table_rows, int max_pages,
+                 int num_pages, int page_size, const int32_t *src, const int32_t *dst, int n,
+                 int32_t *moves, int32_t *count, int32_t *status, void *stream) {
+  if (!kv_ok(table_rows, max_pages, num_pages, page_size) || n < 0 || n > kKvMaxEntries)
+    return COLL_ERR_INVALID_ARG;
+  if (n == 0) return COLL_OK;
+  if (!table || !lens || !ref || !src || !dst || !moves || !count || !status)
+    return COLL_ERR_INVALID_ARG;
+  return launch_kv_fork(launch_ctx(stream), table, lens, ref, table_rows, max_pages, num_pages,
+                        page_size, src, dst, n, moves, count, status);
+}
+
+int coll_kv_free(int32_t *table, int32_t *lens, int32_t *ref, int table_rows, int max_pages,
+                 int num_pages, const int32_t *seqs, int n, void *stream) {
+  if (!kv_ok(table_rows, max_pages, num_pages, 1) || n < 0 || n > kKvMaxEntries)
+    return COLL_ERR_INVALID_ARG;
+  if (n == 0) return COLL_OK;
+  if (!table || !lens || !ref || !seqs) return COLL_ERR_INVALID_ARG;
+  return launch_kv_free(launch_ctx(stream), table, lens, ref, table_rows, max_pages, num_pages,
+                        seqs, n);
+}
+
+size_t coll_kv_compact_workspace_bytes(int num_pages) {
+  if (num_pages < 0 || num_pages > INT32_MAX - 8192) return 0;
+  return ((size_t)num_pages * sizeof(int32_t) + 255) / 256 * 256;
+}
+
+int coll_kv_compact(int32_t *table, int32_t *ref, int table_rows, int max_pages, int num_pages,
+                    int32_t *moves, int max_moves, int32_t *count, void *workspace,
+                    size_t workspace_bytes, void *stream) {
+  if (!kv_ok(table_rows, max_pages, num_pages, 1) || max_moves < num_pages / 2)
+    return COLL_ERR_INVALID_ARG;
+  if (!count || (max_moves > 0 && !moves)) return COLL_ERR_INVALID_ARG;
+  if (((int64_t)table_rows * max_pages > 0 && !table) || (num_pages > 0 && !ref))
+    return COLL_ERR_INVALID_ARG;
+  if (num_pages > 0 && (!workspace || ((uintptr_t)workspace & 255) != 0 ||
+                        workspace_bytes < coll_kv_compact_workspace_bytes(num_pages)))
+    return COLL_ERR_INVALID_ARG;
+  return launch_kv_compact(launch_ctx(stream), table, ref, table_rows, max_pages, num_pages, moves,
+                           max_moves, count, reinterpret_cast<int32_t *>(workspace));
+}
+
+int coll_kv_copy_pages(int npools, void *const *pools, size_t layers, size_t num_pages,
+                       size_t page_bytes, const int32_t *moves, int max_moves,
+                       const int32_t *count, void *stream) {
+  if (!ranks_ok(npools) || max_moves < 0) return COLL_ERR_INVALID_ARG;
+  if (max_moves == 0 || layers == 0 || num_pages == 0 || page_bytes == 0) return COLL_OK;
+  const size_t lim = (size_t)1 << 56;
+  if (layers >= lim / num_pages || page_bytes >= lim / (layers * num_pages) || !moves)
+    return COLL_ERR_INVALID_ARG;
+  MutPtrTable ps{};
+  if (!fill_out(npools, pools, ps.p)) return COLL_ERR_INVALID_ARG;
+  return launch_kv_copy_pages(launch_ctx(stream), npools, ps, layers, num_pages, page_bytes, moves,
+                              max_moves, count);
+}
+
 }  // extern "C"

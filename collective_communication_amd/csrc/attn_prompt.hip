@@ -1,0 +1,402 @@
+// attn_prompt.hip -- attention over packed prompts.
+//
+// Rank r, sequence b with nq query rows and nk key rows, head h of kv head
+// h / (H / KV); key j is visible to query i when j <= i + diag (causal) or
+// always:
+//   s_ij = scale * q_i . k_j,   m_i = max_j s_ij,   p_ij = exp(s_ij - m_i),
+//   l_i = sum_j p_ij,   o_i = sum_j p_ij v_j / l_i,   lse_i = m_i + log l_i,
+// over the visible j.  One pass over the keys in tiles keeps the running m_i
+// and l_i and the unnormalised o_i, which is multiplied by
+// exp(m_old - m_new) when the maximum grows.
+//
+// A workgroup owns NW * 32 query rows of one head, each wave 32 of them.  The
+// wave computes S^T = K Q^T (rows = keys, columns = queries), so a lane holds
+// keys of one query: the row statistics are in-lane reductions plus one
+// exchange between the two halves of the wave, and p, rounded to the input
+// type, is already laid out as the B operand of O^T = V^T P^T.  The fixed
+// permutation of the keys inside 16 that this implies is undone by where V
+// is read: the transposing LDS read takes 4 consecutive keys at a time.
+// K and V tiles are staged through registers into two LDS buffers (one
+// barrier per tile), with 16-byte chunks XOR-swizzled so that neither the
+// row reads of K nor the column reads of V meet bank conflicts.
+#include "matrix.h"
+
+#pragma clang fp contract(off)
+
+namespace coll {
+namespace {
+
+// One call's arguments, by value (1.2 KiB).
+struct PromptArgs {
+  PtrTable q, k, v, q_starts, k_starts, diag;
+  MutPtrTable o, lse;
+  int64_t q_stride, k_stride, v_stride, o_stride;   // elements between tokens
+  int64_t q_rows, k_rows;                           // rows the buffers hold
+  int nseq, heads, kv_heads, causal;
+  uint32_t tiles;                                   // tile slots per (rank, head)
+  FastDiv by_group, by_heads, by_tiles;
+  float c;                                          // |scale| * log2 e
+  int negate;                                       // scale < 0
+};
+
+// Where a workgroup's tile lies.
+struct TileAt {
+  int64_t q0, k0;        // first rows of the sequence
+  int32_t nq, nk, diag;  // its lengths; key j visible to query i when j <= i + diag
+  int32_t first;         // first query row of the tile in the sequence
+  bool any;
+};
+
+// Length of rows [a, b) of a buffer of n rows (0 when they do not all exist).
+__device__ __forceinline__ int32_t span(int64_t a, int64_t b, int64_t n) {
+  return (a < 0 || b <= a || b > n) ? 0 : (int32_t)(b - a);
+}
+
+// The sequence that holds query tile `tile` of rank r: every wave scans the
+// sequences' tile counts, 64 at a time.
+template <int BQ>
+__device__ __forceinline__ TileAt find_tile(const PromptArgs &A, int r, uint32_t tile) {
+  const int32_t *qs = reinterpret_cast<const int32_t *>(A.q_starts.p[r]);
+  const int32_t *ks = reinterpret_cast<const int32_t *>(A.k_starts.p[r]);
+  const int32_t *dg = reinterpret_cast<const int32_t *>(A.diag.p[r]);
+  const int lane = threadIdx.x & 63;
+  TileAt t{};
+  uint32_t before = 0;
+  for (int base = 0; base < A.nseq; base += 64) {
+    const int b = base + lane;
+    int64_t a0 = 0;
+    int32_t nq = 0;
+    if (b < A.nseq) {
+      a0 = qs[b];
+      nq = span(a0, qs[b + 1], A.q_rows);
+    }
+    const uint32_t mine = ((uint32_t)nq + BQ - 1) / BQ;
+    uint32_t upto = mine;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+      const uint32_t x = __shfl_up(upto, d, 64);
+      if (lane >= d) upto += x;
+    }
+    const uint64_t hit = __ballot(before + upto > tile);
+    if (hit) {
+      const int l = __builtin_ctzll(hit);
+      const int bb = base + l;
+      t.any = true;
+      t.first = (int32_t)((tile - before -
+                           (uint32_t)__builtin_amdgcn_readlane((int)(upto - mine), l)) * BQ);
+      t.nq = __builtin_amdgcn_readlane(nq, l);
+      t.q0 = __builtin_amdgcn_readfirstlane(qs[bb]);
+      t.k0 = __builtin_amdgcn_readfirstlane(ks[bb]);
+      const int64_t k1 = __builtin_amdgcn_readfirstlane(ks[bb + 1]);
+      t.nk = span(t.k0, k1, A.k_rows);
+      t.diag = dg ? __builtin_amdgcn_readfirstlane(dg[bb]) : t.nk - t.nq;
+      return t;
+    }
+    before += (uint32_t)__builtin_amdgcn_readlane((int)upto, 63);
+  }
+  return t;
+}
+
+// Chunk swizzles: the LDS position of 16-byte chunk c of row r is c ^ f(r).
+template <int D>
+__device__ __forceinline__ int swz_k(int row) {
+  return D == 96 ? (row >> 1) & 3 : row & 7;
+}
+template <int D>
+__device__ __forceinline__ int swz_v(int row) {
+  return D % 128 == 0 ? (row & 3) << 2 : (D == 96 ? 0 : ((row >> 1) & 1) << 2);
+}
+
+// One tile of BN keys in LDS.
+template <int D, int BN>
+struct Tile {
+  u32x4 k[BN * D / 8];
+  u32x4 v[BN * D / 8];
+};
+
+template <int DT, int D, int BN, int NW>
+__global__ __launch_bounds__(NW * 64, NW == 8 ? 2 : 1) void prompt_tiles(PromptArgs A) {
+  constexpr int BQ = NW * 32, CH = D / 8, NT = NW * 64;
+  constexpr int NCH = (BN * CH + NT - 1) / NT;        // chunks a thread stages of K and of V
+  constexpr bool kWhole = BN * CH % NT == 0;
+  constexpr int DK = D / 16, DV = D / 32, KT = BN / 32;
+  __shared__ __align__(16) Tile<D, BN> s_kv[2];
+  __shared__ int s_bad[2];                            // 1 + index of a tile whose V is not finite
+  // heads vary fastest, and in steps that keep the heads of one kv head on
+  // one XCD (workgroups go round the 8 XCDs); tiles from the last one down,
+  // since causal tiles get longer
+  const uint32_t H = (uint32_t)A.heads;
+  const uint32_t th = fdiv(blockIdx.x, A.by_heads);
+  uint32_t h = blockIdx.x - th * H;
+  if (H % 8 == 0) h = (h & 7) * (H / 8) + (h >> 3);
+  const int r = (int)fdiv(th, A.by_tiles);
+  const uint32_t tile = A.tiles - 1 - (th - (uint32_t)r * A.tiles);
+  const TileAt t = find_tile<BQ>(A, r, tile);
+  if (!t.any) return;
+  const int kvh = (int)fdiv(h, A.by_group);
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int col = lane & 31, g = lane >> 5;
+
+  // keys visible to query row i of the sequence: the first limit(i)
+  auto limit = [&](int i) -> int {
+    if (!A.causal) return t.nk;
+    const int64_t x = (int64_t)i + t.diag + 1;
+    return x < 0 ? 0 : (x > t.nk ? t.nk : (int)x);
+  };
+  const int last_row = (t.first + BQ < t.nq ? t.first + BQ : t.nq) - 1;
+  const int n_block = limit(last_row);                // keys any row of the tile sees
+  const int see_all = limit(t.first);                 // keys every row of the tile sees
+  const int row0 = t.first + wave * 32;               // the wave's rows
+  const int row = row0 + col;
+  const int n_wave = row0 <= last_row ? limit(row0 + 31 < last_row ? row0 + 31 : last_row) : 0;
+  const int all_wave = limit(row0);
+  const int lim = limit(row);
+
+  // Q as the B operand: column = query, 8 consecutive elements per lane
+  u32x4 q[DK];
+  {
+    const char *qp = reinterpret_cast<const char *>(A.q.p[r]) +
+                     ((t.q0 + row) * A.q_stride + (int64_t)h * D) * 2;
+#pragma unroll
+    for (int s = 0; s < DK; s++) {
+      u32x4 x = {0, 0, 0, 0};
+      if (row <= last_row) x = ld<u32x4>(qp, 2 * s + g);
+      if (A.negate) x = x ^ 0x80008000u;
+      q[s] = x;
+    }
+  }
+
+  u32x4 rk[NCH], rv[NCH];
+  const char *kp = reinterpret_cast<const char *>(A.k.p[r]) + (t.k0 * A.k_stride + (int64_t)kvh * D) * 2;
+  const char *vp = reinterpret_cast<const char *>(A.v.p[r]) + (t.k0 * A.v_stride + (int64_t)kvh * D) * 2;
+  auto load_tile = [&](int kt) {
+#pragma unroll
+    for (int i = 0; i < NCH; i++) {
+      const int x = tid + i * NT, kr = x / CH, c = x - kr * CH;
+      const int key = kt * BN + kr;
+      u32x4 a = {0, 0, 0, 0}, b = {0, 0, 0, 0};
+      if ((kWhole || x < BN * CH) && key < t.nk) {
+        a = ld<u32x4>(kp + (int64_t)key * A.k_stride * 2, c);
+        b = ld<u32x4>(vp + (int64_t)key * A.v_stride * 2, c);
+      }
+      rk[i] = a;
+      rv[i] = b;
+    }
+  };
+  auto store_tile = [&](int kt) {
+    Tile<D, BN> &T = s_kv[kt & 1];
+    bool bad = false;
+#pragma unroll
+    for (int i = 0; i < NCH; i++) {
+      const int x = tid + i * NT, kr = x / CH, c = x - kr * CH;
+      if (kWhole || x < BN * CH) {
+        T.k[kr * CH + (c ^ swz_k<D>(kr))] = rk[i];
+        T.v[kr * CH + (c ^ swz_v<D>(kr))] = rv[i];
+      }
+    }
+    // a value that is not finite at a key some row must not see would reach
+    // that row as 0 * inf: such a tile is marked for the careful product
+    if ((kt + 1) * BN > see_all) {
+#pragma unroll
+      for (int i = 0; i < NCH; i++)
+#pragma unroll
+        for (int e = 0; e < 4; e++) bad = bad || pair_not_finite<DT>(rv[i][e]);
+      if (bad) s_bad[kt & 1] = kt + 1;
+    }
+  };
+
+  f32x16 acc[DV];
+#pragma unroll
+  for (int d = 0; d < DV; d++)
+#pragma unroll
+    for (int e = 0; e < 16; e++) acc[d][e] = 0.0f;
+  float m = -__builtin_inff(), l = 0.0f;              // m: running max of s * log2 e / scale units
+
+  const int ntiles = (n_block + BN - 1) / BN;
+  if (tid < 2) s_bad[tid] = 0;
+  if (ntiles > 0) load_tile(0);
+  __syncthreads();
+  if (ntiles > 0) store_tile(0);
+  __syncthreads();
+
+  // V^T as the A operand of rows 32 d.., keys 16 s ..: two transposing reads,
+  // keys 16 s + 4 g + 0..3 and those 8 further on
+  const int vrow = 4 * g + ((lane & 15) >> 2), vcol = (lane & 16) + 4 * (lane & 3);
+  auto v_frag = [&](const Tile<D, BN> &T, int d, int s) -> u32x4 {
+    const int c = (32 * d + vcol) >> 3, half = (lane & 1) * 8;
+    const int r0 = 16 * s + vrow, r1 = r0 + 8;
+    const char *base = reinterpret_cast<const char *>(T.v);
+    const u32x2 x = lds_tr16(base + (r0 * CH + (c ^ swz_v<D>(r0))) * 16 + half);
+    const u32x2 y = lds_tr16(base + (r1 * CH + (c ^ swz_v<D>(r1))) * 16 + half);
+    u32x4 w = {x[0], x[1], y[0], y[1]};
+    return w;
+  };
+
+  for (int kt = 0; kt < ntiles; kt++) {
+    const Tile<D, BN> &T = s_kv[kt & 1];
+    if (kt + 1 < ntiles) load_tile(kt + 1);
+    const int key0 = kt * BN;
+    if (key0 < n_wave) {
+      // S^T, one 32-key tile per accumulator
+      f32x16 s[KT];
+#pragma unroll
+      for (int x = 0; x < KT; x++) {
+#pragma unroll
+        for (int e = 0; e < 16; e++) s[x][e] = 0.0f;
+        const int kr = x * 32 + col;
+#pragma unroll
+        for (int d = 0; d < DK; d++)
+          s[x] = mma32<DT>(T.k[kr * CH + ((2 * d + g) ^ swz_k<D>(kr))], q[d], s[x]);
+      }
+      const bool masked = key0 + BN > all_wave;
+      if (masked) {
+#pragma unroll
+        for (int x = 0; x < KT; x++)
+#pragma unroll
+          for (int e = 0; e < 16; e++) {
+            const int key = key0 + 32 * x + (e & 3) + 8 * (e >> 2) + 4 * g;
+            s[x][e] = key < lim ? s[x][e] : -__builtin_inff();
+          }
+      }
+      // running maximum, in the units of s; it is raised only when it grows
+      // by more than 8 / c (p stays below 2^8), so most tiles rescale nothing
+      float mt = s[0][0];
+#pragma unroll
+      for (int x = 0; x < KT; x++)
+#pragma unroll
+        for (int e = 0; e < 16; e++) mt = fmaxf(mt, s[x][e]);
+      mt = max_halves(mt);
+      if (__ballot((mt - m) * A.c > 8.0f)) {
+        const float mn = fmaxf(m, mt);
+        const float f = mn == -__builtin_inff() ? 1.0f : exp2_f((m - mn) * A.c);
+        m = mn;
+        l *= f;
+#pragma unroll
+        for (int d = 0; d < DV; d++)
+#pragma unroll
+          for (int e = 0; e < 16; e++) acc[d][e] *= f;
+      }
+      const float mc = m == -__builtin_inff() ? 0.0f : m * A.c;
+      u32x4 p[BN / 16];
+#pragma unroll
+      for (int x = 0; x < KT; x++) {
+#pragma unroll
+        for (int e = 0; e < 16; e++) {
+          const float y = exp2_f(__builtin_fmaf(s[x][e], A.c, -mc));
+          l += y;
+          s[x][e] = y;
+        }
+#pragma unroll
+        for (int e = 0; e < 16; e += 2)
+          p[2 * x + (e >> 3)][(e & 7) >> 1] = pack2<DT>(s[x][e], s[x][e + 1]);
+      }
+      if (!masked || s_bad[kt & 1] != kt + 1) {
+#pragma unroll
+        for (int d = 0; d < DV; d++)
+#pragma unroll
+          for (int x = 0; x < BN / 16; x++) acc[d] = mma32<DT>(v_frag(T, d, x), p[x], acc[d]);
+      } else {
+        // key by key, each added only where it is visible
+        for (int j = 0; j < BN; j++) {
+          const int sj = j >> 4, jj = j & 15;
+          // the key's place in the operands: half of the wave and element
+          const int gj = (jj >> 2) & 1, ej = (jj & 3) + 4 * (jj >> 3);
+          const bool mine = g == gj;
+          u32x4 pj = {0, 0, 0, 0};
+#pragma unroll
+          for (int x = 0; x < BN / 16; x++)
+            if (x == sj) pj = p[x];
+          u32x4 keep;
+#pragma unroll
+          for (int w = 0; w < 4; w++)
+            keep[w] = (mine && ej >> 1 == w) ? (ej & 1 ? 0xFFFF0000u : 0xFFFFu) : 0u;
+          pj = pj & keep;
+          const bool vis = key0 + j < lim;
+#pragma unroll
+          for (int d = 0; d < DV; d++) {
+            f32x16 one;
+#pragma unroll
+            for (int e = 0; e < 16; e++) one[e] = 0.0f;
+            one = mma32<DT>(v_frag(T, d, sj) & keep, pj, one);
+#pragma unroll
+            for (int e = 0; e < 16; e++) acc[d][e] += vis ? one[e] : 0.0f;
+          }
+        }
+      }
+    }
+    if (kt + 1 < ntiles) store_tile(kt + 1);
+    __syncthreads();
+  }
+
+  // o = acc / l, lse = m + log l; a row that saw nothing gets 0 and -inf
+  l += lane_xor(l, 32);
+  if (row > last_row) return;
+  const bool none = l == 0.0f;
+  const float inv = none ? 0.0f : 1.0f / l;
+  char *op = reinterpret_cast<char *>(A.o.p[r]) + ((t.q0 + row) * A.o_stride + (int64_t)h * D) * 2;
+#pragma unroll
+  for (int d = 0; d < DV; d++)
+#pragma unroll
+    for (int e = 0; e < 16; e += 4) {
+      float y[4];
+#pragma unroll
+      for (int w = 0; w < 4; w++) y[w] = none ? 0.0f : acc[d][e + w] * inv;
+      u32x2 w2 = {pack2<DT>(y[0], y[1]), pack2<DT>(y[2], y[3])};
+      st<u32x2>(op, (32 * d + 2 * e + 4 * g) / 4, w2);
+    }
+  if (A.lse.p[r] && g == 0)
+    reinterpret_cast<float *>(A.lse.p[r])[(t.q0 + row) * A.heads + h] =
+        none ? -__builtin_inff() : (m * A.c + log2_f(l)) * kLn2;
+}
+
+template <int DT, int D, int BN>
+int go(const Launch &L, int R, PromptArgs &A, int64_t q_rows) {
+  // 8 waves share a staged tile among 256 rows; 4 (128 rows) when that would
+  // leave compute units without a workgroup
+  const uint64_t tiles8 = (uint64_t)(q_rows + 255) / 256 + A.nseq;
+  const bool wide = tiles8 * A.heads * R >= 2ull * L.num_cus;
+  const uint64_t tiles = wide ? tiles8 : (uint64_t)(q_rows + 127) / 128 + A.nseq;
+  const uint64_t groups = tiles * A.heads * R;
+  if (groups > 0x7FFFFFFFull) return COLL_ERR_UNSUPPORTED;
+  A.tiles = (uint32_t)tiles;
+  A.by_tiles = make_fastdiv(A.tiles);
+  if (wide)
+    hipLaunchKernelGGL((prompt_tiles<DT, D, BN, 8>), dim3((unsigned)groups), dim3(512), 0, L.stream, A);
+  else
+    hipLaunchKernelGGL((prompt_tiles<DT, D, BN, 4>), dim3((unsigned)groups), dim3(256), 0, L.stream, A);
+  return hip_status();
+}
+
+}  // namespace
+
+int launch_attn_prompt(const Launch &L, int R, const PtrTable &q, const PtrTable &k,
+                       const PtrTable &v, const MutPtrTable &o, const MutPtrTable &lse,
+                       const PtrTable &q_starts, const PtrTable &k_starts, const PtrTable &diag,
+                       int nseq, int64_t q_rows, int64_t k_rows, int heads, int kv_heads, int D,
+                       int64_t q_stride, int64_t k_stride, int64_t v_stride, int64_t o_stride,
+                       int causal, float scale, int dt) {
+  PromptArgs A{};
+  A.q = q, A.k = k, A.v = v, A.o = o, A.lse = lse;
+  A.q_starts = q_starts, A.k_starts = k_starts, A.diag = diag;
+  A.q_stride = q_stride, A.k_stride = k_stride, A.v_stride = v_stride, A.o_stride = o_stride;
+  A.q_rows = q_rows, A.k_rows = k_rows;
+  A.nseq = nseq, A.heads = heads, A.kv_heads = kv_heads, A.causal = causal;
+  A.by_group = make_fastdiv((uint32_t)(heads / kv_heads));
+  A.by_heads = make_fastdiv((uint32_t)heads);
+  A.negate = scale < 0.0f;
+  A.c = __builtin_fabsf(scale) * kLog2e;
+#define COLL_PROMPT(DTV)                                              \
+  switch (D) {                                                        \
+    case 64: return go<DTV, 64, 64>(L, R, A, q_rows);                 \
+    case 96: return go<DTV, 96, 64>(L, R, A, q_rows);                 \
+    case 128: return go<DTV, 128, 64>(L, R, A, q_rows);               \
+    case 192: return go<DTV, 192, 32>(L, R, A, q_rows);               \
+    case 256: return go<DTV, 256, 32>(L, R, A, q_rows);               \
+    default: return COLL_ERR_UNSUPPORTED;                             \
+  }
+  if (dt == COLL_BF16) { COLL_PROMPT(COLL_BF16) }
+  COLL_PROMPT(COLL_FP16)
+#undef COLL_PROMPT
+}
+
+}  // namespace coll

@@ -562,4 +562,39 @@ int launch_moe_combine_recv(const Launch &L, int R, const PtrTable &recv, const 
                             int K, size_t hidden, const MutPtrTable &out,
                             const RankRows &recv_rows);
 
+int launch_attn_prompt(const Launch &L, int R, const PtrTable &q, const PtrTable &k,
+                       const PtrTable &v, const MutPtrTable &o, const MutPtrTable &lse,
+                       const PtrTable &q_starts, const PtrTable &k_starts, const PtrTable &diag,
+                       int nseq, int64_t q_rows, int64_t k_rows, int heads, int kv_heads, int D,
+                       int64_t q_stride, int64_t k_stride, int64_t v_stride, int64_t o_stride,
+                       int causal, float scale, int dt);
+size_t attn_decode_workspace_bytes(int R, int batch, int64_t max_len, int heads, int kv_heads, int D);
+int launch_attn_decode(const Launch &L, int R, const PtrTable &q, const PtrTable &k,
+                       const PtrTable &v, const PtrTable &table, const PtrTable &lens,
+                       const PtrTable &seqs, const MutPtrTable &o, const MutPtrTable &lse, int batch,
+                       int rows, int max_pages, int64_t num_pages, int page_size, int heads,
+                       int kv_heads, int D, int64_t q_stride, int64_t o_stride, int64_t page_stride,
+                       int64_t tok_stride, int64_t head_stride, float scale, int dt, void *ws);
+int launch_kv_write(const Launch &L, int R, const PtrTable &k, const PtrTable &v,
+                    const MutPtrTable &kp, const MutPtrTable &vp, const PtrTable &table,
+                    const PtrTable &lens, const PtrTable &starts, const PtrTable &seqs,
+                    int64_t tokens, int batch, int rows, int max_pages, int64_t num_pages,
+                    int page_size, int kv_heads, int D, int64_t k_stride, int64_t v_stride,
+                    int64_t page_stride, int64_t tok_stride, int64_t head_stride);
+// entries of one bookkeeping call: one lane each
+constexpr int kKvMaxEntries = COLL_KV_MAX_ENTRIES;
+int launch_kv_extend(const Launch &L, int32_t *table, int32_t *lens, int32_t *ref, int rows,
+                     int width, int num_pages, int page_size, const int32_t *seqs,
+                     const int32_t *add, int n, int32_t *status);
+int launch_kv_fork(const Launch &L, int32_t *table, int32_t *lens, int32_t *ref, int rows,
+                   int width, int num_pages, int page_size, const int32_t *src,
+                   const int32_t *dst, int n, int32_t *moves, int32_t *count, int32_t *status);
+int launch_kv_free(const Launch &L, int32_t *table, int32_t *lens, int32_t *ref, int rows,
+                   int width, int num_pages, const int32_t *seqs, int n);
+int launch_kv_compact(const Launch &L, int32_t *table, int32_t *ref, int rows, int width,
+                      int num_pages, int32_t *moves, int max_moves, int32_t *count, int32_t *map);
+int launch_kv_copy_pages(const Launch &L, int npools, const MutPtrTable &pools, size_t layers,
+                         size_t num_pages, size_t page_bytes, const int32_t *moves, int max_moves,
+                         const int32_t *count);
+
 }  // namespace coll

@@ -561,6 +561,191 @@ int coll_moe_combine_recv(int nranks, const void *const *recvbufs, const int32_t
                           coll_dtype_t dtype, void *const *out, const int64_t *recv_rows,
                           void *stream);
 
+/* ---------------------------------------------------------------------------
+ * Attention and the cache it reads.  The operators on either side of
+ * coll_lse_merge and coll_seq_heads_reshard: they make the partial outputs and
+ * log-sum-exps that the merge joins, over the heads that the re-shard brings
+ * together.  As everywhere, one call serves R ranks (tensor parallel: each
+ * with its heads; context parallel: each with its part of the keys).
+ *
+ * Shared by both attention calls:
+ *  - dtype COLL_BF16 or COLL_FP16; head_dim 64, 96, 128, 192 or 256; others
+ *    COLL_ERR_UNSUPPORTED.  heads is a multiple of kv_heads; query head h
+ *    reads kv head h / (heads / kv_heads).
+ *  - scale multiplies the scores (1 / sqrt(head_dim) as a rule); finite and
+ *    not 0.
+ *  - Scores, softmax statistics and sums are fp32.  The softmax weights are
+ *    rounded to dtype before they multiply the values (at most half a step,
+ *    2^-8 relative for bf16), their sum is taken before that rounding, and
+ *    the output is rounded once more, to nearest even.
+ *  - A row that sees no key, or whose scores are all -inf, gets o = 0 and
+ *    lse = -inf, which coll_lse_merge gives weight 0.  A key that a row does
+ *    not see has no influence on it, whatever it holds (NaN or infinity
+ *    included).
+ *  - lse[r]: fp32 [rows, heads], natural logarithm, may be NULL (as may the
+ *    whole array): not written.
+ *  - Pointers to data are 16-byte aligned and strides (in elements) multiples
+ *    of 8, else COLL_ERR_INVALID_ARG.  Heads are contiguous within a token.
+ *    Outputs must not overlap inputs.
+ * ------------------------------------------------------------------------- */
+
+/*
+ * Attention over packed prompts.  Rank r's sequence b has the query rows
+ * [q_starts[r][b], q_starts[r][b+1]) of q[r] and o[r] and the key rows
+ * [k_starts[r][b], k_starts[r][b+1]) of k[r] and v[r] (DEVICE int32, nseq + 1
+ * entries).  With nq and nk their numbers, query i of the sequence sees key j
+ * if causal is 0, or if j <= i + diag[r][b] (DEVICE int32, nseq entries).
+ * diag NULL means nk - nq: the last query sees all keys.  For a block of a
+ * longer sequence (context parallel), diag is the position of the first query
+ * less that of the first key; it may be negative, or leave rows with no key.
+ *   o_i = sum_j p_ij v_j / sum_j p_ij,  p_ij = exp(scale q_i . k_j - max),
+ *   lse_i = log sum_j exp(scale q_i . k_j), over the keys i sees.
+ *   q[r], o[r]: q_rows tokens of heads * head_dim elements, q_stride and
+ *   o_stride elements apart; k[r], v[r]: k_rows tokens of kv_heads * head_dim.
+ * Rows that belong to no sequence are left as they are.  A sequence whose
+ * query rows do not all lie in [0, q_rows) is not computed; one whose key
+ * rows do not all lie in [0, k_rows) has no keys.
+ * The launch has a workgroup for each 256 (or 128) query rows and one more per
+ * sequence, for each head; q_rows, k_rows < 2^31.
+ */
+int coll_attn_prompt(int nranks, const void *const *q, const void *const *k,
+                     const void *const *v, void *const *o, float *const *lse,
+                     const int32_t *const *q_starts, const int32_t *const *k_starts,
+                     const int32_t *const *diag, int nseq, int64_t q_rows, int64_t k_rows,
+                     int heads, int kv_heads, int head_dim, int64_t q_stride, int64_t k_stride,
+                     int64_t v_stride, int64_t o_stride, int causal, float scale,
+                     coll_dtype_t dtype, void *stream);
+
+/*
+ * Attention of one new token over a paged cache.  Batch entry b of rank r has
+ * the query q[r][b] and the first lens[r][s] tokens of sequence s = seqs[r][b]
+ * (s = b when seqs is NULL; the same sequence may be named more than once) as
+ * keys and values.  Token t of it is slot t % page_size of page
+ * tables[r][s][t / page_size]:
+ *   element e of kv head h at  page * page_stride + slot * tok_stride
+ *                              + h * head_stride + e   of k_pools[r] / v_pools[r].
+ *   tables[r]: DEVICE int32 [table_rows, max_pages]; lens[r]: DEVICE int32
+ *   [table_rows]; seqs[r]: DEVICE int32 [batch].  The strides serve pools laid
+ *   out [page, slot, head, element], [page, head, slot, element], or a layer
+ *   of a larger pool.
+ * Lengths are cut to what a table row can hold; a sequence outside
+ * [0, table_rows) has no tokens; tokens of a page outside [0, num_pages) do
+ * not exist.  So a wrong table can give a wrong result but never touches
+ * memory outside the pools.
+ *   workspace: DEVICE, 256-byte aligned, at least
+ *   coll_attn_decode_workspace_bytes(nranks, batch, max_pages * page_size,
+ *   heads, kv_heads, head_dim) bytes; overwritten, needs no initial value, and
+ *   concurrent calls need workspaces of their own.
+ * The cache is read once per 16 query heads of a kv head.  Equal shares of all
+ * entries' tokens go to the workgroups, whatever the lengths, and a second
+ * kernel joins what was split; the result does not depend on timing.
+ * Errors: COLL_ERR_UNSUPPORTED also for max_pages * page_size near or over 2^31.
+ */
+size_t coll_attn_decode_workspace_bytes(int nranks, int batch, int64_t max_len, int heads,
+                                        int kv_heads, int head_dim);
+int coll_attn_decode(int nranks, const void *const *q, const void *const *k_pools,
+                     const void *const *v_pools, const int32_t *const *tables,
+                     const int32_t *const *lens, const int32_t *const *seqs, void *const *o,
+                     float *const *lse, int batch, int table_rows, int max_pages,
+                     int64_t num_pages, int page_size, int heads, int kv_heads, int head_dim,
+                     int64_t q_stride, int64_t o_stride, int64_t page_stride, int64_t tok_stride,
+                     int64_t head_stride, float scale, coll_dtype_t dtype, void *workspace,
+                     size_t workspace_bytes, void *stream);
+
+/*
+ * Write new tokens' keys and values into the cache.  Rows
+ * [starts[r][b], starts[r][b+1]) of k[r] and v[r] (packed tokens of
+ * kv_heads * head_dim elements, k_stride / v_stride elements apart; starts:
+ * DEVICE int32 [batch + 1]) are the LAST tokens of sequence s = seqs[r][b] (b
+ * when seqs is NULL): row t goes to position lens[r][s] - (starts[r][b+1] - t).
+ * Call it after coll_kv_extend has grown the sequences.  Pools, tables, lens
+ * and seqs as in coll_attn_decode; any 16-bit dtype, head_dim a multiple of 8
+ * up to 1024.  Rows of no sequence, and rows whose position or page does not
+ * exist, are not written.  Two batch entries must not name one sequence.
+ */
+int coll_kv_write(int nranks, const void *const *k, const void *const *v, void *const *k_pools,
+                  void *const *v_pools, const int32_t *const *tables, const int32_t *const *lens,
+                  const int32_t *const *starts, const int32_t *const *seqs, int64_t tokens,
+                  int batch, int table_rows, int max_pages, int64_t num_pages, int page_size,
+                  int kv_heads, int head_dim, int64_t k_stride, int64_t v_stride,
+                  int64_t page_stride, int64_t tok_stride, int64_t head_stride,
+                  coll_dtype_t dtype, void *stream);
+
+/* ---------------------------------------------------------------------------
+ * Pages of a cache, managed on the device (no call needs a host
+ * synchronisation).  State, all DEVICE int32:
+ *   table[table_rows][max_pages]: page of each page_size tokens of a sequence,
+ *   -1 for none; lens[table_rows]: its tokens (0: the row is empty);
+ *   ref[num_pages]: table entries that name the page, 0 for a free one.
+ * Start with table = -1, lens = 0, ref = 0.  Ranks that hold the same
+ * sequences (tensor parallel) share one state; ranks with their own parts of
+ * the keys (context parallel) have one each.  Calls on one state must be
+ * ordered (one stream, or events).  Fresh pages are the lowest free ones, dealt to
+ * the entries in list order, so the results are determined by the state.
+ * A call takes at most COLL_KV_MAX_ENTRIES entries (n; 0 is a no-op).
+ *   status[i] (DEVICE int32 [n]): 0 = done, -1 = the entry is not valid,
+ *   -2 = too few free pages: the pages wanted by the valid entries up to and
+ *   including this one exceed them.  An entry that is not done changes nothing.
+ * A page other than the last of a sequence is full and never written again,
+ * so sharing it is safe; a partly filled one has a single owner.
+ * ------------------------------------------------------------------------- */
+#define COLL_KV_MAX_ENTRIES 1024
+
+/*
+ * Grow sequences: lens[seqs[i]] += add[i], with fresh pages for what does not
+ * fit the last one (ref = 1).  Not valid: a row outside the table, one that an
+ * earlier entry names, add < 0, or more tokens than a table row can hold.
+ */
+int coll_kv_extend(int32_t *table, int32_t *lens, int32_t *ref, int table_rows, int max_pages,
+                   int num_pages, int page_size, const int32_t *seqs, const int32_t *add, int n,
+                   int32_t *status, void *stream);
+
+/*
+ * Fork: the empty row dst[i] becomes a copy of row src[i] as it is when the
+ * call begins.  It shares the full pages (ref + 1) and gets a fresh page for a
+ * partly filled last one: moves[k] = (from, to) (DEVICE int32 [n][2]), k
+ * counting these copies in list order, *count (DEVICE int32) of them, the
+ * rest -1.  Pass moves and count to coll_kv_copy_pages before the pages are
+ * read.  The same source may be named many times.  Not valid: rows outside
+ * the table, src[i] == dst[i], a destination that is not empty or that an
+ * earlier entry names.
+ */
+int coll_kv_fork(int32_t *table, int32_t *lens, int32_t *ref, int table_rows, int max_pages,
+                 int num_pages, int page_size, const int32_t *src, const int32_t *dst, int n,
+                 int32_t *moves, int32_t *count, int32_t *status, void *stream);
+
+/*
+ * Free the sequences seqs[i]: their pages' ref falls by 1, their rows become
+ * empty.  Rows outside the table and rows an earlier entry names are skipped.
+ */
+int coll_kv_free(int32_t *table, int32_t *lens, int32_t *ref, int table_rows, int max_pages,
+                 int num_pages, const int32_t *seqs, int n, void *stream);
+
+/*
+ * Compact: with c pages in use, the k-th page in use at or above c moves to the
+ * k-th free page below c, so that the pages in use become 0 .. c - 1.  Rewrites
+ * table and ref and lists the copies: moves[k] = (from, to), *count of them,
+ * the rest -1 (DEVICE int32 [max_moves][2], max_moves >= num_pages / 2).  Pass
+ * them to coll_kv_copy_pages for every pool before the pages are read.
+ *   workspace: DEVICE, 256-byte aligned, coll_kv_compact_workspace_bytes bytes.
+ */
+size_t coll_kv_compact_workspace_bytes(int num_pages);
+int coll_kv_compact(int32_t *table, int32_t *ref, int table_rows, int max_pages, int num_pages,
+                    int32_t *moves, int max_moves, int32_t *count, void *workspace,
+                    size_t workspace_bytes, void *stream);
+
+/*
+ * Copy pages: for m < *count (or max_moves if count is NULL), page moves[m][1]
+ * of every pool and layer gets the bytes of page moves[m][0].  pools: npools
+ * (1 .. COLL_MAX_RANKS) contiguous buffers [layers][num_pages][page_bytes]
+ * (for instance the K and V pools of each rank).  Pairs with an index outside
+ * [0, num_pages) are skipped; a page must not be both a source and a
+ * destination, nor a destination twice (the lists above never do that).
+ */
+int coll_kv_copy_pages(int npools, void *const *pools, size_t layers, size_t num_pages,
+                       size_t page_bytes, const int32_t *moves, int max_moves,
+                       const int32_t *count, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -14,6 +14,7 @@
 // filled with a poison pattern before each workgroup.
 #include <stdio.h>
 #include <stdlib.h>
+#include <string.h>
 #include <sys/mman.h>
 #include <ucontext.h>
 
@@ -72,6 +73,40 @@ bool same_site(const Lane &a, const Lane &b) {
   return a.op == b.op && a.line == b.line && strcmp(a.file, b.file) == 0;
 }
 
+float emu_half(uint16_t x, int dt) {
+  if (dt == 0) {
+    const uint32_t b = (uint32_t)x << 16;
+    float f;
+    memcpy(&f, &b, 4);
+    return f;
+  }
+  _Float16 h;
+  memcpy(&h, &x, 2);
+  return (float)h;
+}
+
+// One matrix instruction of a whole wave, in the layout that the library's
+// matrix.h documents; the sums run over k in ascending order in fp32.
+void do_matrix(Lane *w) {
+  emu_matrix *m[64];
+  for (int l = 0; l < 64; l++) m[l] = (emu_matrix *)(uintptr_t)w[l].val;
+  const int side = m[0]->wide ? 32 : 16, groups = 64 / side, K = groups * 8;
+  static float a[32][32], b[32][32];
+  for (int l = 0; l < 64; l++)
+    for (int j = 0; j < 8; j++) {
+      a[l % side][8 * (l / side) + j] = emu_half(m[l]->a[j], m[l]->dt);
+      b[l % side][8 * (l / side) + j] = emu_half(m[l]->b[j], m[l]->dt);
+    }
+  const int nr = m[0]->wide ? 16 : 4;
+  for (int l = 0; l < 64; l++)
+    for (int r = 0; r < nr; r++) {
+      const int row = m[0]->wide ? r % 4 + 8 * (r / 4) + 4 * (l / 32) : 4 * (l / 16) + r;
+      float c = m[l]->c[r];
+      for (int k = 0; k < K; k++) c += a[row][k] * b[l % side][k];
+      m[l]->c[r] = c;
+    }
+}
+
 void resolve_wave(Lane *w, int n) {
   int op = 0, first_lane = -1;
   uint64_t active = 0;
@@ -88,6 +123,10 @@ void resolve_wave(Lane *w, int n) {
     active |= 1ull << l;
   }
   int first = __builtin_ctzll(active);
+  if (op == EMU_MATRIX || op == EMU_LDS_TR16) {
+    if (n != 64 || active != ~0ull) die("matrix operation without all 64 lanes");
+    if (op == EMU_MATRIX) do_matrix(w);
+  }
   for (int l = 0; l < n; l++) {
     if (!((active >> l) & 1)) continue;
     Lane &x = w[l];
@@ -126,6 +165,19 @@ void resolve_wave(Lane *w, int n) {
         // source lane's value is not modelled, so it is an error here
         if (!((active >> src) & 1)) die("readlane of an inactive lane");
         x.result = w[src].val;
+        break;
+      }
+      case EMU_MATRIX:
+        x.result = 0;
+        break;
+      case EMU_LDS_TR16: {
+        // lane i of a group of 16 gets column i of the rows that lanes
+        // 4 j .. 4 j + 3 read, j = 0..3
+        const int g = l & ~15, i = l & 15;
+        uint64_t r = 0;
+        for (int j = 0; j < 4; j++)
+          r |= ((w[g + 4 * j + i / 4].val >> (16 * (i & 3))) & 0xFFFF) << (16 * j);
+        x.result = r;
         break;
       }
       default:

@@ -87,7 +87,16 @@ static inline hipError_t hipGetSymbolAddress(void **p, const void *sym) {
 // (slots, ranks and descriptors loaded from one address), and a lane that
 // disagreed would go on with lane 0's address on the GPU.
 enum { EMU_BALLOT = 1, EMU_SHFL = 2, EMU_SHFL_UP = 3, EMU_FIRSTLANE = 4, EMU_READLANE = 5,
-       EMU_UNIFORM = 6 };
+       EMU_UNIFORM = 6, EMU_MATRIX = 7, EMU_LDS_TR16 = 8 };
+
+// Operands of one lane of a matrix instruction (EMU_MATRIX), passed by the
+// address of this record: the whole wave must take part.
+struct emu_matrix {
+  int dt;               // 0 = bf16, 1 = fp16
+  int wide;             // 1: 32x32x16, 0: 16x16x32
+  uint16_t a[8], b[8];
+  float c[16];
+};
 
 template <class T>
 static inline uint64_t emu_bits(T v) {
@@ -138,6 +147,67 @@ static inline int emu_readlane_at(int v, int lane, const char *f, int l) {
 #define __builtin_amdgcn_readfirstlane(v) emu_readfirstlane_at((int)(v), __FILE__, __LINE__)
 #define __builtin_amdgcn_readlane(v, l) emu_readlane_at((int)(v), (int)(l), __FILE__, __LINE__)
 
+// --------------------------------------------------- matrix.h's helpers
+// The library's matrix.h leaves these to the including environment when
+// COLL_HAVE_MATRIX is defined; layouts as documented there.
+#define COLL_HAVE_MATRIX 1
+typedef uint32_t emu_u32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t emu_u32x2 __attribute__((ext_vector_type(2)));
+typedef float emu_f32x4 __attribute__((ext_vector_type(4)));
+typedef float emu_f32x16 __attribute__((ext_vector_type(16)));
+
+template <int DT, int WIDE, int NR, class C>
+static inline C emu_mma(emu_u32x4 a, emu_u32x4 b, C c, const char *f, int l) {
+  emu_matrix m;
+  m.dt = DT;
+  m.wide = WIDE;
+  for (int i = 0; i < 4; i++) {
+    m.a[2 * i] = (uint16_t)a[i];
+    m.a[2 * i + 1] = (uint16_t)(a[i] >> 16);
+    m.b[2 * i] = (uint16_t)b[i];
+    m.b[2 * i + 1] = (uint16_t)(b[i] >> 16);
+  }
+  for (int i = 0; i < NR; i++) m.c[i] = c[i];
+  emu_wave_op(EMU_MATRIX, (uint64_t)(uintptr_t)&m, 0, f, l);
+  for (int i = 0; i < NR; i++) c[i] = m.c[i];
+  return c;
+}
+template <int DT>
+static inline emu_f32x16 emu_mma32(emu_u32x4 a, emu_u32x4 b, emu_f32x16 c, const char *f, int l) {
+  return emu_mma<DT, 1, 16>(a, b, c, f, l);
+}
+template <int DT>
+static inline emu_f32x4 emu_mma16(emu_u32x4 a, emu_u32x4 b, emu_f32x4 c, const char *f, int l) {
+  return emu_mma<DT, 0, 4>(a, b, c, f, l);
+}
+template <int DT>
+static inline emu_f32x16 mma32(emu_u32x4 a, emu_u32x4 b, emu_f32x16 c,
+                               const char *f = __builtin_FILE(), int l = __builtin_LINE()) {
+  return emu_mma32<DT>(a, b, c, f, l);
+}
+template <int DT>
+static inline emu_f32x4 mma16(emu_u32x4 a, emu_u32x4 b, emu_f32x4 c,
+                              const char *f = __builtin_FILE(), int l = __builtin_LINE()) {
+  return emu_mma16<DT>(a, b, c, f, l);
+}
+static inline emu_u32x2 lds_tr16(const void *p, const char *f = __builtin_FILE(),
+                                 int l = __builtin_LINE()) {
+  uint64_t v;
+  memcpy(&v, p, 8);
+  const uint64_t r = emu_wave_op(EMU_LDS_TR16, v, 0, f, l);
+  emu_u32x2 x = {(uint32_t)r, (uint32_t)(r >> 32)};
+  return x;
+}
+static inline float exp2_f(float x) { return exp2f(x); }
+static inline float log2_f(float x) { return log2f(x); }
+static inline float max_halves(float x, const char *f = __builtin_FILE(), int l = __builtin_LINE()) {
+  const int other = (int)(emu_thread_idx()->x & 63) ^ 32;
+  return fmaxf(x, emu_shfl_at(x, other, 64, f, l));
+}
+struct int4 {
+  int x, y, z, w;
+};
+
 // ------------------------------------------------------------ integer helpers
 static inline int __popcll(unsigned long long x) { return __builtin_popcountll(x); }
 static inline int __popc(unsigned x) { return __builtin_popcount(x); }
@@ -152,6 +222,12 @@ template <class T>
 static inline T atomicAdd(T *p, T v) {
   T old = *p;
   *p = old + v;
+  return old;
+}
+template <class T>
+static inline T atomicMax(T *p, T v) {
+  T old = *p;
+  if (v > old) *p = v;
   return old;
 }
 
