@@ -122,9 +122,11 @@ __global__ __launch_bounds__(256, 2) void decode_split(DecodeArgs A) {
     base = 0;
     scan(0);
   }
-  const int W = (int)gridDim.x, w0 = (int)blockIdx.x;
-  int u = share(total, w0, W);
-  const int u1 = share(total, w0 + 1, W), begin = u;
+  // as many workgroups share the units as there are units, so that each of
+  // them has one and the joined partials are those of consecutive workgroups
+  const int W = (int)gridDim.x < total ? (int)gridDim.x : total, w0 = (int)blockIdx.x;
+  int u = w0 < W ? share(total, w0, W) : 0;
+  const int u1 = w0 < W ? share(total, w0 + 1, W) : 0, begin = u;
   int4 join = {0, 0, 0, 0};
 
   while (u < u1) {

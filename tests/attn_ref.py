@@ -128,9 +128,9 @@ def check(name, got_o, got_lse, o, lse, to, tl, dtype):
         if not (np.array_equal(np.isnan(x), np.isnan(y)) and
                 np.array_equal(x[~fine & ~np.isnan(y)], y[~fine & ~np.isnan(y)])):
             raise AssertionError(f"{name} {what}: not finite at other places")
-        over = np.abs(x - y)[fine] - t[fine]
-        if over.size and over.max() > 0:
-            i = np.argmax(np.where(fine, np.abs(x - y) - t, -np.inf))
+        d = np.where(fine, np.abs(np.where(fine, x, 0.0) - np.where(fine, y, 0.0)) - t, -np.inf)
+        if d.size and d.max() > 0:
+            i = np.argmax(d)
             at = np.unravel_index(i, x.shape)
             raise AssertionError(f"{name} {what}: {x[at]} for {y[at]} at {at}, allowed {t[at]}")
 

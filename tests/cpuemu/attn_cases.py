@@ -174,7 +174,8 @@ def decode_case(name, R, heads, kv, D, lens, P, *, dtype="bf16", width=None, seq
         lo.append(H.empty((B, heads), np.float32))
         lo[-1][...] = 7.0
         sqs.append(None if sq is None else H.copy(sq))
-    ws = H.poison(cases.L.coll_attn_decode_workspace_bytes(R, B, width * P, heads, kv, D), np.uint8)
+    ws = H.empty(cases.L.coll_attn_decode_workspace_bytes(R, B, width * P, heads, kv, D), np.uint8)
+    ws[...] = 0xFF                                       # NaN
     ok(cases.L.coll_attn_decode(
         R, table(qs), table(ks), table(vs), table(ts), table(ls), None if seqs is None else table(sqs),
         table(os_), table(lo) if lse else None, B, S, width, N, P, heads, kv, D, heads * D + pad,
