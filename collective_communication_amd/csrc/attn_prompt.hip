@@ -17,11 +17,16 @@
 // permutation of the keys inside 16 that this implies is undone by where V
 // is read: the transposing LDS read takes 4 consecutive keys at a time.
 // K and V tiles are staged through registers into two LDS buffers (one
-// barrier per tile), with 16-byte chunks XOR-swizzled so that neither the
-// row reads of K nor the column reads of V meet bank conflicts.
+// barrier per tile).
 #include "matrix.h"
 
 #pragma clang fp contract(off)
+#ifndef COLL_PROMPT_OCC
+#define COLL_PROMPT_OCC (NW == 8 ? 2 : 1)
+#endif
+#ifndef COLL_PROMPT_WIDE
+#define COLL_PROMPT_WIDE 1
+#endif
 
 namespace coll {
 namespace {
@@ -97,30 +102,26 @@ __device__ __forceinline__ TileAt find_tile(const PromptArgs &A, int r, uint32_t
   return t;
 }
 
-// Chunk swizzles: the LDS position of 16-byte chunk c of row r is c ^ f(r).
-template <int D>
-__device__ __forceinline__ int swz_k(int row) {
-  return D == 96 ? (row >> 1) & 3 : row & 7;
-}
-template <int D>
-__device__ __forceinline__ int swz_v(int row) {
-  return D % 128 == 0 ? (row & 3) << 2 : (D == 96 ? 0 : ((row >> 1) & 1) << 2);
-}
-
-// One tile of BN keys in LDS.
+// BN keys in LDS, two tiles of K and two of V.  The rows are padded so that
+// neither the row reads of K (8 lanes, 16 bytes of 8 consecutive rows: a
+// stride of 4 mod 32 banks) nor the column reads of V (32 lanes, 64 bytes of
+// 4 consecutive rows: 16 or 48 mod 64 banks) meet bank conflicts; a lane's
+// address is then one base and a constant.
 template <int D, int BN>
-struct Tile {
-  u32x4 k[BN * D / 8];
-  u32x4 v[BN * D / 8];
+struct Tiles {
+  static constexpr int kRowK = D + 8, kRowV = D % 64 == 0 ? D + 32 : D;   // elements
+  uint16_t k[2][BN * kRowK];
+  uint16_t v[2][BN * kRowV];
 };
 
 template <int DT, int D, int BN, int NW>
-__global__ __launch_bounds__(NW * 64, NW == 8 ? 2 : 1) void prompt_tiles(PromptArgs A) {
+__global__ __launch_bounds__(NW * 64, COLL_PROMPT_OCC) void prompt_tiles(PromptArgs A) {
   constexpr int BQ = NW * 32, CH = D / 8, NT = NW * 64;
   constexpr int NCH = (BN * CH + NT - 1) / NT;        // chunks a thread stages of K and of V
   constexpr bool kWhole = BN * CH % NT == 0;
   constexpr int DK = D / 16, DV = D / 32, KT = BN / 32;
-  __shared__ __align__(16) Tile<D, BN> s_kv[2];
+  using TL = Tiles<D, BN>;
+  __shared__ __align__(16) TL s_t;
   __shared__ int s_bad[2];                            // 1 + index of a tile whose V is not finite
   // heads vary fastest, and in steps that keep the heads of one kv head on
   // one XCD (workgroups go round the 8 XCDs); tiles from the last one down,
@@ -149,7 +150,6 @@ __global__ __launch_bounds__(NW * 64, NW == 8 ? 2 : 1) void prompt_tiles(PromptA
   const int row0 = t.first + wave * 32;               // the wave's rows
   const int row = row0 + col;
   const int n_wave = row0 <= last_row ? limit(row0 + 31 < last_row ? row0 + 31 : last_row) : 0;
-  const int all_wave = limit(row0);
   const int lim = limit(row);
 
   // Q as the B operand: column = query, 8 consecutive elements per lane
@@ -166,37 +166,41 @@ __global__ __launch_bounds__(NW * 64, NW == 8 ? 2 : 1) void prompt_tiles(PromptA
     }
   }
 
+  // a thread's chunks of a tile: key kr0[i] of the tile, 16 bytes at chunk c
   u32x4 rk[NCH], rv[NCH];
   const char *kp = reinterpret_cast<const char *>(A.k.p[r]) + (t.k0 * A.k_stride + (int64_t)kvh * D) * 2;
   const char *vp = reinterpret_cast<const char *>(A.v.p[r]) + (t.k0 * A.v_stride + (int64_t)kvh * D) * 2;
-  auto load_tile = [&](int kt) {
+  auto load_one = [&](u32x4 (&dst)[NCH], const char *src, int64_t stride, int kt) {
 #pragma unroll
     for (int i = 0; i < NCH; i++) {
       const int x = tid + i * NT, kr = x / CH, c = x - kr * CH;
       const int key = kt * BN + kr;
-      u32x4 a = {0, 0, 0, 0}, b = {0, 0, 0, 0};
-      if ((kWhole || x < BN * CH) && key < t.nk) {
-        a = ld<u32x4>(kp + (int64_t)key * A.k_stride * 2, c);
-        b = ld<u32x4>(vp + (int64_t)key * A.v_stride * 2, c);
-      }
-      rk[i] = a;
-      rv[i] = b;
+      u32x4 a = {0, 0, 0, 0};
+      if ((kWhole || x < BN * CH) && key < t.nk) a = ld<u32x4>(src + key * stride * 2, c);
+      dst[i] = a;
     }
   };
-  auto store_tile = [&](int kt) {
-    Tile<D, BN> &T = s_kv[kt & 1];
-    bool bad = false;
+  auto load_k = [&](int kt) { load_one(rk, kp, A.k_stride, kt); };
+  auto load_v = [&](int kt) { load_one(rv, vp, A.v_stride, kt); };
+  auto store_k = [&](int kt) {
 #pragma unroll
     for (int i = 0; i < NCH; i++) {
       const int x = tid + i * NT, kr = x / CH, c = x - kr * CH;
-      if (kWhole || x < BN * CH) {
-        T.k[kr * CH + (c ^ swz_k<D>(kr))] = rk[i];
-        T.v[kr * CH + (c ^ swz_v<D>(kr))] = rv[i];
-      }
+      if (kWhole || x < BN * CH)
+        *reinterpret_cast<u32x4 *>(s_t.k[kt & 1] + kr * TL::kRowK + 8 * c) = rk[i];
+    }
+  };
+  auto store_v = [&](int kt) {
+#pragma unroll
+    for (int i = 0; i < NCH; i++) {
+      const int x = tid + i * NT, kr = x / CH, c = x - kr * CH;
+      if (kWhole || x < BN * CH)
+        *reinterpret_cast<u32x4 *>(s_t.v[kt & 1] + kr * TL::kRowV + 8 * c) = rv[i];
     }
     // a value that is not finite at a key some row must not see would reach
     // that row as 0 * inf: such a tile is marked for the careful product
     if ((kt + 1) * BN > see_all) {
+      bool bad = false;
 #pragma unroll
       for (int i = 0; i < NCH; i++)
 #pragma unroll
@@ -210,91 +214,138 @@ __global__ __launch_bounds__(NW * 64, NW == 8 ? 2 : 1) void prompt_tiles(PromptA
   for (int d = 0; d < DV; d++)
 #pragma unroll
     for (int e = 0; e < 16; e++) acc[d][e] = 0.0f;
-  float m = -__builtin_inff(), l = 0.0f;              // m: running max of s * log2 e / scale units
+  // m: running maximum, in the units of the unscaled scores; l: this lane's
+  // part of the sum, in two
+  float m = -__builtin_inff(), l0 = 0.0f, l1 = 0.0f;
 
-  const int ntiles = (n_block + BN - 1) / BN;
-  if (tid < 2) s_bad[tid] = 0;
-  if (ntiles > 0) load_tile(0);
-  __syncthreads();
-  if (ntiles > 0) store_tile(0);
-  __syncthreads();
-
+  // S^T of a tile, 32 keys per accumulator
+  const int kat = col * TL::kRowK + 8 * g;
+  auto scores = [&](int kt, f32x16 (&s)[KT]) {
+    const uint16_t *base = s_t.k[kt & 1] + kat;
+#pragma unroll
+    for (int x = 0; x < KT; x++)
+#pragma unroll
+      for (int e = 0; e < 16; e++) s[x][e] = 0.0f;
+#pragma unroll
+    for (int d = 0; d < DK; d++)
+#pragma unroll
+      for (int x = 0; x < KT; x++)
+        s[x] = mma32<DT>(*reinterpret_cast<const u32x4 *>(base + x * 32 * TL::kRowK + 16 * d), q[d], s[x]);
+  };
   // V^T as the A operand of rows 32 d.., keys 16 s ..: two transposing reads,
   // keys 16 s + 4 g + 0..3 and those 8 further on
-  const int vrow = 4 * g + ((lane & 15) >> 2), vcol = (lane & 16) + 4 * (lane & 3);
-  auto v_frag = [&](const Tile<D, BN> &T, int d, int s) -> u32x4 {
-    const int c = (32 * d + vcol) >> 3, half = (lane & 1) * 8;
-    const int r0 = 16 * s + vrow, r1 = r0 + 8;
-    const char *base = reinterpret_cast<const char *>(T.v);
-    const u32x2 x = lds_tr16(base + (r0 * CH + (c ^ swz_v<D>(r0))) * 16 + half);
-    const u32x2 y = lds_tr16(base + (r1 * CH + (c ^ swz_v<D>(r1))) * 16 + half);
+  const int vat = (4 * g + ((lane & 15) >> 2)) * TL::kRowV + (lane & 16) + 4 * (lane & 3);
+  auto v_frag = [&](int kt, int d, int s) -> u32x4 {
+    const uint16_t *p = s_t.v[kt & 1] + vat + 16 * s * TL::kRowV + 32 * d;
+    const u32x2 x = lds_tr16(p), y = lds_tr16(p + 8 * TL::kRowV);
     u32x4 w = {x[0], x[1], y[0], y[1]};
     return w;
   };
+  // The maximum is raised only when it grows by more than 8 / c (p stays below
+  // 2^8), so most tiles rescale nothing.
+  auto raise = [&](const f32x16 (&s)[KT]) {
+    float a = s[0][0], b = s[0][1];
+#pragma unroll
+    for (int x = 0; x < KT; x++)
+#pragma unroll
+      for (int e = x == 0 ? 2 : 0; e < 16; e += 2) {
+        a = fmaxf(a, s[x][e]);
+        b = fmaxf(b, s[x][e + 1]);
+      }
+    const float mt = max_halves(fmaxf(a, b));
+    if (__ballot((mt - m) * A.c > 8.0f)) {
+      const float mn = fmaxf(m, mt);
+      const float f = mn == -__builtin_inff() ? 1.0f : exp2_f((m - mn) * A.c);
+      m = mn;
+      l0 *= f;
+      l1 *= f;
+#pragma unroll
+      for (int d = 0; d < DV; d++)
+#pragma unroll
+        for (int e = 0; e < 16; e++) acc[d][e] *= f;
+    }
+  };
+  auto weights = [&](const f32x16 (&s)[KT], u32x4 (&p)[BN / 16]) {
+    const float mc = m == -__builtin_inff() ? 0.0f : m * A.c;
+#pragma unroll
+    for (int x = 0; x < KT; x++)
+#pragma unroll
+      for (int e = 0; e < 16; e += 2) {
+        const float y0 = exp2_f(__builtin_fmaf(s[x][e], A.c, -mc));
+        const float y1 = exp2_f(__builtin_fmaf(s[x][e + 1], A.c, -mc));
+        l0 += y0;
+        l1 += y1;
+        p[2 * x + (e >> 3)][(e & 7) >> 1] = pack2<DT>(y0, y1);
+      }
+  };
 
-  for (int kt = 0; kt < ntiles; kt++) {
-    const Tile<D, BN> &T = s_kv[kt & 1];
-    if (kt + 1 < ntiles) load_tile(kt + 1);
+  const int ntiles = (n_block + BN - 1) / BN;
+  const int nfull = see_all / BN < ntiles ? see_all / BN : ntiles;   // tiles that need no mask
+  if (tid < 2) s_bad[tid] = 0;
+  if (ntiles > 0) {
+    load_k(0);
+    load_v(0);
+  }
+  __syncthreads();
+  if (ntiles > 0) {
+    store_k(0);
+    store_v(0);
+    if (ntiles > 1) {
+      load_k(1);
+      store_k(1);
+    }
+  }
+  __syncthreads();
+
+  // The scores of the next tile are computed with the weights of this one, so
+  // that a wave has matrix work while it computes exponentials: K is staged
+  // a tile further ahead than V.  One barrier per tile: what is written was
+  // last read before the previous one.
+  f32x16 s[KT];
+  const bool busy = n_wave > 0;
+  if (busy) scores(0, s);
+  __syncthreads();
+  int kt = 0;
+  for (; kt < nfull; kt++) {
+    if (kt + 2 < ntiles) load_k(kt + 2);
+    if (kt + 1 < ntiles) load_v(kt + 1);
+    if (busy) {
+      raise(s);
+      u32x4 p[BN / 16];
+      f32x16 nx[KT];
+      weights(s, p);
+      scores(kt + 1, nx);                             // of an old tile after the last one: not used
+#pragma unroll
+      for (int x = 0; x < BN / 16; x++)
+#pragma unroll
+        for (int d = 0; d < DV; d++) acc[d] = mma32<DT>(v_frag(kt, d, x), p[x], acc[d]);
+#pragma unroll
+      for (int x = 0; x < KT; x++) s[x] = nx[x];
+    }
+    if (kt + 2 < ntiles) store_k(kt + 2);
+    if (kt + 1 < ntiles) store_v(kt + 1);
+    __syncthreads();
+  }
+  for (; kt < ntiles; kt++) {                         // tiles on the diagonal and the last one
+    if (kt + 2 < ntiles) load_k(kt + 2);
+    if (kt + 1 < ntiles) load_v(kt + 1);
     const int key0 = kt * BN;
     if (key0 < n_wave) {
-      // S^T, one 32-key tile per accumulator
-      f32x16 s[KT];
-#pragma unroll
-      for (int x = 0; x < KT; x++) {
-#pragma unroll
-        for (int e = 0; e < 16; e++) s[x][e] = 0.0f;
-        const int kr = x * 32 + col;
-#pragma unroll
-        for (int d = 0; d < DK; d++)
-          s[x] = mma32<DT>(T.k[kr * CH + ((2 * d + g) ^ swz_k<D>(kr))], q[d], s[x]);
-      }
-      const bool masked = key0 + BN > all_wave;
-      if (masked) {
-#pragma unroll
-        for (int x = 0; x < KT; x++)
-#pragma unroll
-          for (int e = 0; e < 16; e++) {
-            const int key = key0 + 32 * x + (e & 3) + 8 * (e >> 2) + 4 * g;
-            s[x][e] = key < lim ? s[x][e] : -__builtin_inff();
-          }
-      }
-      // running maximum, in the units of s; it is raised only when it grows
-      // by more than 8 / c (p stays below 2^8), so most tiles rescale nothing
-      float mt = s[0][0];
 #pragma unroll
       for (int x = 0; x < KT; x++)
 #pragma unroll
-        for (int e = 0; e < 16; e++) mt = fmaxf(mt, s[x][e]);
-      mt = max_halves(mt);
-      if (__ballot((mt - m) * A.c > 8.0f)) {
-        const float mn = fmaxf(m, mt);
-        const float f = mn == -__builtin_inff() ? 1.0f : exp2_f((m - mn) * A.c);
-        m = mn;
-        l *= f;
-#pragma unroll
-        for (int d = 0; d < DV; d++)
-#pragma unroll
-          for (int e = 0; e < 16; e++) acc[d][e] *= f;
-      }
-      const float mc = m == -__builtin_inff() ? 0.0f : m * A.c;
-      u32x4 p[BN / 16];
-#pragma unroll
-      for (int x = 0; x < KT; x++) {
-#pragma unroll
         for (int e = 0; e < 16; e++) {
-          const float y = exp2_f(__builtin_fmaf(s[x][e], A.c, -mc));
-          l += y;
-          s[x][e] = y;
+          const int key = key0 + 32 * x + (e & 3) + 8 * (e >> 2) + 4 * g;
+          s[x][e] = key < lim ? s[x][e] : -__builtin_inff();
         }
+      raise(s);
+      u32x4 p[BN / 16];
+      weights(s, p);
+      if (s_bad[kt & 1] != kt + 1) {
 #pragma unroll
-        for (int e = 0; e < 16; e += 2)
-          p[2 * x + (e >> 3)][(e & 7) >> 1] = pack2<DT>(s[x][e], s[x][e + 1]);
-      }
-      if (!masked || s_bad[kt & 1] != kt + 1) {
+        for (int x = 0; x < BN / 16; x++)
 #pragma unroll
-        for (int d = 0; d < DV; d++)
-#pragma unroll
-          for (int x = 0; x < BN / 16; x++) acc[d] = mma32<DT>(v_frag(T, d, x), p[x], acc[d]);
+          for (int d = 0; d < DV; d++) acc[d] = mma32<DT>(v_frag(kt, d, x), p[x], acc[d]);
       } else {
         // key by key, each added only where it is visible
         for (int j = 0; j < BN; j++) {
@@ -317,16 +368,19 @@ __global__ __launch_bounds__(NW * 64, NW == 8 ? 2 : 1) void prompt_tiles(PromptA
             f32x16 one;
 #pragma unroll
             for (int e = 0; e < 16; e++) one[e] = 0.0f;
-            one = mma32<DT>(v_frag(T, d, sj) & keep, pj, one);
+            one = mma32<DT>(v_frag(kt, d, sj) & keep, pj, one);
 #pragma unroll
             for (int e = 0; e < 16; e++) acc[d][e] += vis ? one[e] : 0.0f;
           }
         }
       }
+      if (key0 + BN < n_wave) scores(kt + 1, s);
     }
-    if (kt + 1 < ntiles) store_tile(kt + 1);
+    if (kt + 2 < ntiles) store_k(kt + 2);
+    if (kt + 1 < ntiles) store_v(kt + 1);
     __syncthreads();
   }
+  float l = l0 + l1;
 
   // o = acc / l, lse = m + log l; a row that saw nothing gets 0 and -inf
   l += lane_xor(l, 32);
@@ -354,7 +408,7 @@ int go(const Launch &L, int R, PromptArgs &A, int64_t q_rows) {
   // 8 waves share a staged tile among 256 rows; 4 (128 rows) when that would
   // leave compute units without a workgroup
   const uint64_t tiles8 = (uint64_t)(q_rows + 255) / 256 + A.nseq;
-  const bool wide = tiles8 * A.heads * R >= 2ull * L.num_cus;
+  const bool wide = COLL_PROMPT_WIDE && tiles8 * A.heads * R >= 2ull * L.num_cus;
   const uint64_t tiles = wide ? tiles8 : (uint64_t)(q_rows + 127) / 128 + A.nseq;
   const uint64_t groups = tiles * A.heads * R;
   if (groups > 0x7FFFFFFFull) return COLL_ERR_UNSUPPORTED;
