@@ -6,20 +6,24 @@
 //   o = sum p_t v_t / l,    lse = m + log l.
 // Token t lies in page table[row][t / P] at slot t % P.
 //
-// The keys and values are read once, and that is what bounds it.  The work
-// is one list of units of 128 tokens of one (rank, entry, kv head), and
-// every workgroup takes an equal, contiguous share of it, whatever the
-// lengths: long caches are split among many workgroups, short ones share
-// one.  A workgroup that holds all units of a head writes its output;
-// otherwise it leaves its partial (m, l, unnormalised o) in the workspace
-// and a second kernel joins the partials.
+// The keys and values are read once, and that is what bounds it.  The caches
+// of all (rank, entry) pairs are one list of units of 128 tokens, cut into
+// equal contiguous shares whatever the lengths: long caches are split among
+// many workgroups, short ones share one.  A share is taken by one workgroup
+// per head (16 query heads of one kv head), next to each other, so that
+// those that run together read the neighbouring heads of the same tokens.
+// A workgroup that holds all units of an entry writes its output; otherwise it
+// leaves its partial (m, l, unnormalised o) in the workspace and a second
+// kernel joins the partials.
 //
-// A wave takes 32 tokens at a time, straight from memory to the registers
-// the matrix instructions read.  S = K Q^T has a token per row and a head
-// per column; the rows are dealt so that a lane ends with 8 consecutive
-// tokens of one head, which is how the B operand of O^T = V^T P^T wants
-// them.  V's operand holds 8 tokens of one column per lane: a lane loads
-// the same few columns of 8 tokens and transposes the block in registers.
+// A wave takes 32 tokens at a time; every load covers whole rows (16 lanes a
+// row), since halves of a cache line asked for one after the other cost a
+// tenth of the bandwidth.  S = K Q^T has a token per row and a head per
+// column; the rows are dealt so that a lane ends with 8 consecutive tokens of
+// one head, which is how the B operand of O^T = V^T P^T wants them.  K gets
+// into its operand's layout through a piece of LDS of the wave's own; V's
+// operand holds 8 tokens of one column per lane, and a lane that has loaded
+// the same few columns of 8 tokens transposes the block in registers.
 #include "matrix.h"
 
 #pragma clang fp contract(off)
@@ -29,7 +33,9 @@ namespace {
 
 constexpr int kUnit = 128;            // tokens of one unit: 32 for each of 4 waves
 constexpr int kHeadTile = 16;         // query heads of one kv head that share a pass
+constexpr int kMaxSplit = 512;        // workgroups of the split (more only if there are more heads)
 constexpr int kJoinLanes = 512;
+constexpr int kFewPartials = 8;       // joined by one wave
 
 struct DecodeArgs {
   PtrTable q, k, v, table, lens, seqs;
@@ -40,11 +46,12 @@ struct DecodeArgs {
   int batch, rows, max_pages, page_size;
   int heads, kv_heads, group, head_tiles;           // head_tiles per kv head
   int entries;                                      // ranks * batch
-  FastDiv by_batch, by_page, by_head_tiles;
+  FastDiv by_batch, by_page, by_head_tiles, by_wide;
   float c;                                          // |scale| * log2 e
   int negate;
   float *part;                                      // partial slots, two per workgroup
-  int4 *joins;                                      // per workgroup: {partials, first slot, entry, head tile}
+  int4 *joins;                                      // per workgroup: {partials, first slot, entry, -}
+  int heads_wide;                                   // kv_heads * head_tiles: workgroups per share
 };
 
 // Floats of one partial slot: the outputs, then m and l per head.
@@ -66,35 +73,64 @@ __device__ __forceinline__ int entry_len(const DecodeArgs &A, int e, int *row) {
 }
 __device__ __forceinline__ int units_of(int len) { return len > 0 ? (len + kUnit - 1) / kUnit : 1; }
 
-// First unit of workgroup w's share of n units among `of` workgroups.
+// First unit of share w of n units in `of` shares.
 __device__ __forceinline__ int share(int64_t n, int w, int of) { return (int)(n * w / of); }
 
+// ND consecutive dwords, non-temporal: the cache is read once (64 ragged caches
+// of 583 MB: 106 us against 120 with plain loads; 128 MB: 34 against 38).
 template <int ND>
-struct Chunk {                 // 32 tokens of one wave, as loaded
-  u32x4 k[2][ND];
-  uint32_t v[8][ND];
+__device__ __forceinline__ void ld_row(const char *p, uint32_t (&x)[ND]) {
+  constexpr int N = ND % 4 == 0 ? 4 : (ND % 2 == 0 ? 2 : 1);
+  typedef uint32_t piece __attribute__((ext_vector_type(N), aligned(4)));
+#pragma unroll
+  for (int h = 0; h < ND / N; h++) {
+    const piece v = __builtin_nontemporal_load(reinterpret_cast<const piece *>(p) + h);
+#pragma unroll
+    for (int i = 0; i < N; i++) x[h * N + i] = v[i];
+  }
+}
+
+template <int ND>
+struct Chunk {                 // 32 tokens of one wave, as loaded: lane 16 g + i has
+  uint32_t k[8][ND];           // ND dwords from dword i ND on of the rows of tokens
+  uint32_t v[8][ND];           // 8 g + j
   uint32_t ok;                 // bit j: token 8 g + j of the chunk exists
 };
 
 template <int DT, int ND, bool P8>
 __global__ __launch_bounds__(256, 2) void decode_split(DecodeArgs A) {
-  constexpr int D = 32 * ND, NV = P8 ? 1 : 8, NK = P8 ? 1 : 2;
+  constexpr int D = 32 * ND, NV = P8 ? 1 : 8;
   constexpr int kOutRow = D + 4;
-  constexpr bool kAhead = ND <= 4;      // two chunks in registers: 64 of them each at D = 128
-  __shared__ int s_pre[257], s_wave[4];
+  __shared__ int s_pre[257], s_len[256], s_row[256], s_wave[4];
   __shared__ float s_m[4][kHeadTile], s_l[4][kHeadTile];
-  __shared__ __align__(16) float s_o[4][kHeadTile][kOutRow];
+  // per wave: K of a chunk, rows in operand order and padded (a stride of 4 mod
+  // 32 banks), and after the last chunk the wave's outputs
+  constexpr int kKeyRow = 16 * ND + 4;                // dwords
+  union Own {
+    uint32_t k[32 * kKeyRow];
+    float o[kHeadTile][kOutRow];
+  };
+  __shared__ __align__(16) Own s_own[4];
+  constexpr bool kQueryLds = ND > 6;
+  __shared__ __align__(16) u32x4 s_q[kQueryLds ? ND : 1][64];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int i16 = lane & 15, g = lane >> 4;
-  const int per_entry = A.kv_heads * A.head_tiles;
+  const int w0 = (int)fdiv(blockIdx.x, A.by_wide), ht = (int)blockIdx.x - w0 * A.heads_wide;
+  const int shares = (int)fdiv(gridDim.x, A.by_wide);
+  const int kvh = (int)fdiv((uint32_t)ht, A.by_head_tiles), part = ht - kvh * A.head_tiles;
+  const int h0 = kvh * A.group + part * kHeadTile;
+  const int nh = A.group - part * kHeadTile < kHeadTile ? A.group - part * kHeadTile : kHeadTile;
 
   // prefix sums of the entries' units, 256 entries at a time: s_pre[i] = units
-  // before entry base + i (all head tiles together)
+  // before entry base + i
   int base = 0;
   auto scan = [&](int carry) {
     const int e = base + tid;
-    int row;
-    const int mine = e < A.entries ? units_of(entry_len(A, e, &row)) * per_entry : 0;
+    int row = 0, len = 0, mine = 0;
+    if (e < A.entries) {
+      len = entry_len(A, e, &row);
+      mine = units_of(len);
+    }
     int upto = mine;
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) {
@@ -108,6 +144,8 @@ __global__ __launch_bounds__(256, 2) void decode_split(DecodeArgs A) {
 #pragma unroll
     for (int w = 0; w < 3; w++) before += w < wave ? s_wave[w] : 0;
     s_pre[tid + 1] = before + upto;
+    s_len[tid] = len;
+    s_row[tid] = row;
     if (tid == 0) s_pre[0] = carry;
     __syncthreads();
   };
@@ -122,9 +160,9 @@ __global__ __launch_bounds__(256, 2) void decode_split(DecodeArgs A) {
     base = 0;
     scan(0);
   }
-  // as many workgroups share the units as there are units, so that each of
-  // them has one and the joined partials are those of consecutive workgroups
-  const int W = (int)gridDim.x < total ? (int)gridDim.x : total, w0 = (int)blockIdx.x;
+  // at most as many shares as there are units, so that each has one and the
+  // joined partials are those of consecutive shares
+  const int W = shares < total ? shares : total;
   int u = w0 < W ? share(total, w0, W) : 0;
   const int u1 = w0 < W ? share(total, w0 + 1, W) : 0, begin = u;
   int4 join = {0, 0, 0, 0};
@@ -142,20 +180,18 @@ __global__ __launch_bounds__(256, 2) void decode_split(DecodeArgs A) {
       if (s_pre[mid] <= u) lo = mid;
       else hi = mid;
     }
-    const int e = __builtin_amdgcn_readfirstlane(base + lo);
-    int row_v;
-    const int len = __builtin_amdgcn_readfirstlane(entry_len(A, e, &row_v));
-    const int trow = __builtin_amdgcn_readfirstlane(row_v);
+    lo = __builtin_amdgcn_readfirstlane(lo);
+    const int e = base + lo;
+    const int len = __builtin_amdgcn_readfirstlane(s_len[lo]);
+    const int trow = __builtin_amdgcn_readfirstlane(s_row[lo]);
     const int nu = units_of(len);
-    const int local = u - s_pre[lo], ht = local / nu, t0 = local - ht * nu;
+    const int t0 = u - __builtin_amdgcn_readfirstlane(s_pre[lo]);
     const int t1 = nu < t0 + (u1 - u) ? nu : t0 + (u1 - u);
     const int r = (int)fdiv((uint32_t)e, A.by_batch), b = e - r * A.batch;
-    const int kvh = (int)fdiv((uint32_t)ht, A.by_head_tiles), part = ht - kvh * A.head_tiles;
-    const int h0 = kvh * A.group + part * kHeadTile;
-    const int nh = A.group - part * kHeadTile < kHeadTile ? A.group - part * kHeadTile : kHeadTile;
 
-    // Q as the B operand: column = head, 8 consecutive elements per lane
-    u32x4 q[ND];
+    // Q as the B operand: column = head, 8 consecutive elements per lane; kept
+    // in LDS where the registers would not hold it too
+    u32x4 q[kQueryLds ? 1 : ND];
 #pragma unroll
     for (int s = 0; s < ND; s++) {
       u32x4 x = {0, 0, 0, 0};
@@ -163,30 +199,26 @@ __global__ __launch_bounds__(256, 2) void decode_split(DecodeArgs A) {
         x = ld<u32x4>(reinterpret_cast<const char *>(A.q.p[r]) +
                           (b * A.q_stride + (int64_t)(h0 + i16) * D) * 2, 4 * s + g);
       if (A.negate) x = x ^ 0x80008000u;
-      q[s] = x;
+      if constexpr (!kQueryLds) q[s] = x;
+      else if (wave == 0) s_q[s][lane] = x;
     }
+    if constexpr (kQueryLds) __syncthreads();
     const char *kp = reinterpret_cast<const char *>(A.k.p[r]) + (int64_t)kvh * A.head_stride * 2;
     const char *vp = reinterpret_cast<const char *>(A.v.p[r]) + (int64_t)kvh * A.head_stride * 2;
     const int32_t *pages = reinterpret_cast<const int32_t *>(A.table.p[r]) +
                            (len > 0 ? (int64_t)trow * A.max_pages : 0);
 
-    // Tokens of a chunk that starts at token `at`: operand row i of K's tile
-    // m is token 8 (i / 4) + 4 m + i % 4; V's elements are tokens 8 g + j.
-    // With pages of a multiple of 8 tokens, 8 of them share one look-up.
+    // Pages of the lane's tokens 8 g + j of the chunk at `at`: one look-up where
+    // pages are a multiple of 8 tokens.
     struct Look {
-      int32_t v[NV], k[NK];
+      int32_t page[NV];
     };
     auto look = [&](int at) -> Look {
       Look x;
 #pragma unroll
       for (int j = 0; j < NV; j++) {
         const int t = at + 8 * g + j;
-        x.v[j] = t < len ? pages[fdiv((uint32_t)t, A.by_page)] : -1;
-      }
-#pragma unroll
-      for (int m = 0; m < NK; m++) {
-        const int t = at + 8 * (i16 >> 2) + (P8 ? 0 : 4 * m + (i16 & 3));
-        x.k[m] = t < len ? pages[fdiv((uint32_t)t, A.by_page)] : -1;
+        x.page[j] = t < len ? pages[fdiv((uint32_t)t, A.by_page)] : -1;
       }
       return x;
     };
@@ -197,24 +229,14 @@ __global__ __launch_bounds__(256, 2) void decode_split(DecodeArgs A) {
       Chunk<ND> ch;
       ch.ok = 0;
 #pragma unroll
-      for (int m = 0; m < 2; m++) {
-        const int t = at + 8 * (i16 >> 2) + 4 * m + (i16 & 3);
-        const int32_t pg = x.k[P8 ? 0 : m];
-        const bool ok = t < len && pg >= 0 && pg < A.num_pages;
-        const int64_t off = ok ? pg * A.page_stride + slot_of(t) * A.tok_stride : 0;
-#pragma unroll
-        for (int s = 0; s < ND; s++) ch.k[m][s] = ld<u32x4>(kp + off * 2, 4 * s + g);
-      }
-#pragma unroll
       for (int j = 0; j < 8; j++) {
         const int t = at + 8 * g + j;
-        const int32_t pg = x.v[P8 ? 0 : j];
+        const int32_t pg = x.page[P8 ? 0 : j];
         const bool ok = t < len && pg >= 0 && pg < A.num_pages;
-        const int64_t off = ok ? pg * A.page_stride + slot_of(t) * A.tok_stride : 0;
-        const uint32_t *src = reinterpret_cast<const uint32_t *>(vp + off * 2) + i16 * ND;
-#pragma unroll
-        for (int x2 = 0; x2 < ND; x2++) ch.v[j][x2] = src[x2];
+        const int64_t off = (ok ? pg * A.page_stride + slot_of(t) * A.tok_stride : 0) * 2 + i16 * (4 * ND);
         ch.ok |= ok ? 1u << j : 0u;
+        ld_row<ND>(kp + off, ch.k[j]);
+        ld_row<ND>(vp + off, ch.v[j]);
       }
       return ch;
     };
@@ -225,13 +247,26 @@ __global__ __launch_bounds__(256, 2) void decode_split(DecodeArgs A) {
     float m = -__builtin_inff(), l = 0.0f;
 
     auto compute = [&](Chunk<ND> &ch) {
+      // row i of K's operand x is token 8 (i / 4) + 4 x + i % 4; a wave's LDS
+      // accesses are in order, so its own piece needs no barrier
+#pragma unroll
+      for (int j = 0; j < 8; j++) {
+        uint32_t *row = s_own[wave].k + (16 * (j >> 2) + 4 * g + (j & 3)) * kKeyRow + i16 * ND;
+#pragma unroll
+        for (int x = 0; x < ND; x++) row[x] = ch.k[j][x];
+      }
+      wave_lds_sync();
       f32x4 s[2];
 #pragma unroll
       for (int x = 0; x < 2; x++) {
         s[x] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-        for (int d = 0; d < ND; d++) s[x] = mma16<DT>(ch.k[x][d], q[d], s[x]);
+        for (int d = 0; d < ND; d++)
+          s[x] = mma16<DT>(*reinterpret_cast<const u32x4 *>(s_own[wave].k + (16 * x + i16) * kKeyRow +
+                                                            16 * d + 4 * g),
+                         kQueryLds ? s_q[d][lane] : q[kQueryLds ? 0 : d], s[x]);
       }
+      wave_lds_sync();
       if (__ballot(ch.ok != 0xFFu)) {
 #pragma unroll
         for (int j = 0; j < 8; j++) {
@@ -279,33 +314,17 @@ __global__ __launch_bounds__(256, 2) void decode_split(DecodeArgs A) {
       }
     };
 
-    // the wave's chunks: tokens 128 t + 32 wave .., loads one chunk ahead of
-    // the arithmetic and page look-ups one further
+    // the wave's chunks, 128 tokens apart.  Page look-ups run one ahead; the
+    // loads do not (with two workgroups on a compute unit there are enough in
+    // flight: a second chunk in registers measured 1% slower).
     const int stop = len < t1 * kUnit ? len : t1 * kUnit;
     int at = t0 * kUnit + wave * 32;
     if (at < stop) {
       Look nxt = look(at);
-      if constexpr (kAhead) {
+      for (; at < stop; at += kUnit) {
         Chunk<ND> cur = load(at, nxt);
         nxt = look(at + kUnit);
-        for (;;) {
-          const bool more = at + kUnit < stop;
-          Chunk<ND> ahead;
-          if (more) {
-            ahead = load(at + kUnit, nxt);
-            nxt = look(at + 2 * kUnit);
-          }
-          compute(cur);
-          if (!more) break;
-          cur = ahead;
-          at += kUnit;
-        }
-      } else {
-        for (; at < stop; at += kUnit) {
-          Chunk<ND> cur = load(at, nxt);
-          nxt = look(at + kUnit);
-          compute(cur);
-        }
+        compute(cur);
       }
     }
 
@@ -325,11 +344,11 @@ __global__ __launch_bounds__(256, 2) void decode_split(DecodeArgs A) {
 #pragma unroll
       for (int rr = 0; rr < 4; rr++)
 #pragma unroll
-        for (int x = 0; x < 2 * ND; x++) s_o[wave][i16][2 * ND * (4 * g + rr) + x] = acc[x][rr] * f;
+        for (int x = 0; x < 2 * ND; x++) s_own[wave].o[i16][2 * ND * (4 * g + rr) + x] = acc[x][rr] * f;
     }
     __syncthreads();
     const bool whole = t0 == 0 && t1 == nu;
-    const int slot = 2 * w0 + (u == begin ? 0 : 1);
+    const int slot = 2 * (int)blockIdx.x + (u == begin ? 0 : 1);
     float *ps = A.part + (int64_t)slot * slot_floats<D>();
     for (int x = tid; x < nh * (D / 2); x += 256) {
       const int hh = x / (D / 2), d = 2 * (x - hh * (D / 2));
@@ -341,8 +360,8 @@ __global__ __launch_bounds__(256, 2) void decode_split(DecodeArgs A) {
       for (int w = 0; w < 4; w++) {
         const float mw = s_m[w][hh], lw = s_l[w][hh];
         ll += mw == -__builtin_inff() ? (lw != lw ? lw : 0.0f) : lw * exp2_f((mw - M) * A.c);
-        y0 += s_o[w][hh][d];
-        y1 += s_o[w][hh][d + 1];
+        y0 += s_own[w].o[hh][d];
+        y1 += s_own[w].o[hh][d + 1];
       }
       if (whole) {
         const bool none = ll == 0.0f;
@@ -362,100 +381,174 @@ __global__ __launch_bounds__(256, 2) void decode_split(DecodeArgs A) {
       }
     }
     if (t0 == 0 && !whole) {
-      // the head's units end in another workgroup: that many partials follow
+      // the entry's units end in another share: that many partials
       int64_t last = (int64_t)u + nu - 1;
       int w = (int)(last * W / total);
       while (share(total, w + 1, W) <= last) w++;
-      join = int4{w - w0 + 1, slot, e, ht};
+      join = int4{w - w0 + 1, slot, e, 0};
     }
     __syncthreads();
     u += t1 - t0;
   }
-  if (tid == 0) A.joins[w0] = join;
+  if (tid == 0) A.joins[blockIdx.x] = join;
 }
 
-// One workgroup per (workgroup of the split, head of the tile): if that
-// workgroup began a head that others went on with, join the partials.  Its
-// own slot comes first, then slot 0 of each workgroup after it.
+// One workgroup per (workgroup of the split, head of its 16): if that workgroup
+// began an entry that later shares went on with, join the partials.  Its own
+// slot comes first, then slot 0 of the same heads' workgroup of each share
+// after it.
 template <int DT, int ND>
 __global__ __launch_bounds__(kJoinLanes) void decode_join(DecodeArgs A) {
-  constexpr int D = 32 * ND, NW = kJoinLanes / 64, PL = (D + 63) / 64;
-  __shared__ float s_l[NW], s_o[NW][D];
-  const int w0 = (int)blockIdx.x, hh = (int)blockIdx.y;
-  const int4 join = A.joins[w0];
+  constexpr int D = 32 * ND, NW = kJoinLanes / 64;
+  constexpr int LR = D / 4, RW = kJoinLanes / LR;     // lanes of a row (4 floats each), rows at a time
+  __shared__ float s_f[kMaxSplit], s_m[NW], s_l[NW];
+  __shared__ __align__(16) f32x4 s_o[RW][LR];
+  const int hh = (int)blockIdx.y;
+  const int4 join = A.joins[blockIdx.x];
   const int n = __builtin_amdgcn_readfirstlane(join.x);
   if (n == 0) return;
-  const int e = join.z, ht = join.w;
+  const int e = join.z, ht = (int)(blockIdx.x - fdiv(blockIdx.x, A.by_wide) * A.heads_wide);
   const int r = (int)fdiv((uint32_t)e, A.by_batch), b = e - r * A.batch;
   const int kvh = (int)fdiv((uint32_t)ht, A.by_head_tiles), part = ht - kvh * A.head_tiles;
   const int nh = A.group - part * kHeadTile < kHeadTile ? A.group - part * kHeadTile : kHeadTile;
   if (hh >= nh) return;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   auto slot_at = [&](int i) -> const float * {
-    return A.part + (int64_t)(i == 0 ? join.y : 2 * (w0 + i)) * slot_floats<D>();
+    return A.part + (int64_t)(i == 0 ? join.y : 2 * ((int)blockIdx.x + i * A.heads_wide)) * slot_floats<D>();
   };
-  // every wave finds the maximum of all partials, then sums its share
-  float M = -__builtin_inff();
-  for (int i = lane; i < n; i += 64) M = fmaxf(M, slot_at(i)[kHeadTile * D + hh]);
+  const int h = kvh * A.group + part * kHeadTile + hh;
+  char *op = reinterpret_cast<char *>(A.o.p[r]) + (b * A.o_stride + (int64_t)h * D) * 2;
+  float *lp = reinterpret_cast<float *>(A.lse.p[r]);
+  if (n <= kFewPartials) {
+    // the common case in a batch: one wave, no barrier, all rows in flight
+    if (wave > 0) return;
+    float m1 = -__builtin_inff(), l1 = 0.0f;
+    if (lane < n) {
+      m1 = slot_at(lane)[kHeadTile * D + hh];
+      l1 = slot_at(lane)[kHeadTile * D + kHeadTile + hh];
+    }
+    constexpr int PL = (D / 2 + 63) / 64;             // pairs of a lane
+    f32x2 v[kFewPartials][PL];
 #pragma unroll
-  for (int d = 1; d < 64; d <<= 1) M = fmaxf(M, lane_xor(M, d));
-  float y[PL], ll = 0.0f;
+    for (int i = 0; i < kFewPartials; i++)
 #pragma unroll
-  for (int x = 0; x < PL; x++) y[x] = 0.0f;
-#pragma unroll 4
-  for (int i = wave; i < n; i += NW) {
-    const float *s = slot_at(i);
-    const float mi = s[kHeadTile * D + hh], li = s[kHeadTile * D + kHeadTile + hh];
-    const float f = mi == -__builtin_inff() ? (li != li ? li : 0.0f) : exp2_f((mi - M) * A.c);
-    ll += li * f;
+      for (int x = 0; x < PL; x++) {
+        v[i][x] = f32x2{0.0f, 0.0f};
+        const int d = 2 * (x * 64 + lane);
+        if (i < n && d < D) v[i][x] = *reinterpret_cast<const f32x2 *>(slot_at(i) + hh * D + d);
+      }
+    float M1 = m1;
+#pragma unroll
+    for (int d = 1; d < kFewPartials; d <<= 1) M1 = fmaxf(M1, lane_xor(M1, d));
+    M1 = __shfl(M1, 0, 64);
+    const float f1 = m1 == -__builtin_inff() ? (l1 != l1 ? l1 : 0.0f) : exp2_f((m1 - M1) * A.c);
+    float L1 = l1 * f1;
+#pragma unroll
+    for (int d = 1; d < kFewPartials; d <<= 1) L1 += lane_xor(L1, d);
+    L1 = __shfl(L1, 0, 64);
+    const bool none = L1 == 0.0f;
+    const float inv = none ? 0.0f : 1.0f / L1;
+    float y[PL][2] = {};
+#pragma unroll
+    for (int i = 0; i < kFewPartials; i++) {
+      const float w = __shfl(f1, i, 64);
+      if (i < n)
+#pragma unroll
+        for (int x = 0; x < PL; x++) {
+          y[x][0] += v[i][x][0] * w;
+          y[x][1] += v[i][x][1] * w;
+        }
+    }
 #pragma unroll
     for (int x = 0; x < PL; x++) {
-      const int d = x * 64 + lane;
-      if (D % 64 == 0 || d < D) y[x] += s[hh * D + d] * f;
+      const int d = 2 * (x * 64 + lane);
+      if (d < D)
+        *reinterpret_cast<uint32_t *>(op + 2 * d) = none ? 0u : pack2<DT>(y[x][0] * inv, y[x][1] * inv);
     }
+    if (lane == 0 && lp)
+      lp[(int64_t)b * A.heads + h] = none ? -__builtin_inff() : (M1 * A.c + log2_f(L1)) * kLn2;
+    return;
   }
+  // a lane per partial (n <= kMaxSplit): its weight exp2((m_i - m) c)
+  static_assert(kMaxSplit <= kJoinLanes, "a lane per partial");
+  float mi = -__builtin_inff(), li = 0.0f;
+  if (tid < n) {
+    mi = slot_at(tid)[kHeadTile * D + hh];
+    li = slot_at(tid)[kHeadTile * D + kHeadTile + hh];
+  }
+  float M = mi;
 #pragma unroll
-  for (int x = 0; x < PL; x++) {
-    const int d = x * 64 + lane;
-    if (D % 64 == 0 || d < D) s_o[wave][d] = y[x];
-  }
-  if (lane == 0) s_l[wave] = ll;
+  for (int d = 1; d < 64; d <<= 1) M = fmaxf(M, lane_xor(M, d));
+  if (lane == 0) s_m[wave] = M;
   __syncthreads();
-  const int h = kvh * A.group + part * kHeadTile + hh;
-  float L = 0.0f;
+  M = s_m[0];
+#pragma unroll
+  for (int w = 1; w < NW; w++) M = fmaxf(M, s_m[w]);
+  const float f = mi == -__builtin_inff() ? (li != li ? li : 0.0f) : exp2_f((mi - M) * A.c);
+  if (tid < n) s_f[tid] = f;
+  float L = li * f;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) L += lane_xor(L, d);
+  if (lane == 0) s_l[wave] = L;
+  __syncthreads();
+  L = 0.0f;
 #pragma unroll
   for (int w = 0; w < NW; w++) L += s_l[w];
+  // the rows, RW at a time and 8 of each lane's in flight
+  const int rw = tid / LR, c = tid - rw * LR;
+  f32x4 y = {0.0f, 0.0f, 0.0f, 0.0f};
+  if (rw < RW) {
+    for (int i0 = rw; i0 < n; i0 += 8 * RW) {
+      f32x4 v[8];
+      float w[8];
+#pragma unroll
+      for (int j = 0; j < 8; j++) {
+        const int i = i0 + j * RW < n ? i0 + j * RW : i0;
+        v[j] = *reinterpret_cast<const f32x4 *>(slot_at(i) + hh * D + 4 * c);
+        w[j] = i0 + j * RW < n ? s_f[i] : 0.0f;
+      }
+#pragma unroll
+      for (int j = 0; j < 8; j++)
+        if (i0 + j * RW < n)
+#pragma unroll
+          for (int x = 0; x < 4; x++) y[x] += v[j][x] * w[j];
+    }
+    s_o[rw][c] = y;
+  }
+  __syncthreads();
+  if (tid >= LR) return;
+  y = s_o[0][tid];
+#pragma unroll
+  for (int i = 1; i < RW; i++)
+#pragma unroll
+    for (int x = 0; x < 4; x++) y[x] += s_o[i][tid][x];
   const bool none = L == 0.0f;
   const float inv = none ? 0.0f : 1.0f / L;
-  for (int d = 2 * threadIdx.x; d < D; d += 2 * kJoinLanes) {
-    float a = 0.0f, c = 0.0f;
-#pragma unroll
-    for (int w = 0; w < NW; w++) {
-      a += s_o[w][d];
-      c += s_o[w][d + 1];
-    }
-    char *op = reinterpret_cast<char *>(A.o.p[r]) + (b * A.o_stride + (int64_t)h * D + d) * 2;
-    *reinterpret_cast<uint32_t *>(op) = none ? 0u : pack2<DT>(a * inv, c * inv);
-  }
-  if (threadIdx.x == 0 && A.lse.p[r])
-    reinterpret_cast<float *>(A.lse.p[r])[(int64_t)b * A.heads + h] =
-        none ? -__builtin_inff() : (M * A.c + log2_f(L)) * kLn2;
+  u32x2 w2 = {pack2<DT>(y[0] * inv, y[1] * inv), pack2<DT>(y[2] * inv, y[3] * inv)};
+  if (none) w2 = u32x2{0u, 0u};
+  st<u32x2>(op, tid, w2);
+  if (tid == 0 && lp)
+    lp[(int64_t)b * A.heads + h] = none ? -__builtin_inff() : (M * A.c + log2_f(L)) * kLn2;
 }
 
-// Workgroups of the split: one per unit that may exist, 512 at most (two of
-// 4 waves on each of 256 compute units).
-constexpr int kMaxSplit = 512;
+// Workgroups of the split: 512 (two of 4 waves on each of 256 compute units),
+// in whole shares of one per 16 heads, and no more shares than there may be
+// units.
 
-int64_t unit_bound(int R, int batch, int64_t max_len, int heads, int kv_heads) {
-  const int64_t tiles = (heads / kv_heads + kHeadTile - 1) / kHeadTile;
+int64_t unit_bound(int R, int batch, int64_t max_len) {
   const int64_t per = max_len > 0 ? (max_len + kUnit - 1) / kUnit : 1;
-  return (int64_t)R * batch * kv_heads * tiles * per;
+  return (int64_t)R * batch * per;
 }
-int split_of(int64_t units) { return (int)(units < kMaxSplit ? units : kMaxSplit); }
+int64_t wide_of(int heads, int kv_heads) {
+  return (int64_t)kv_heads * ((heads / kv_heads + kHeadTile - 1) / kHeadTile);
+}
+int64_t split_of(int64_t units, int64_t wide) {
+  const int64_t most = wide < kMaxSplit ? kMaxSplit / wide : 1;
+  return wide * (units < most ? units : most);
+}
 
 template <int DT, int ND>
-int go(const Launch &L, const DecodeArgs &A, int64_t units, bool splits) {
-  const int W = split_of(units);
+int go(const Launch &L, const DecodeArgs &A, int W, bool splits) {
   if (A.page_size % 8 == 0)
     hipLaunchKernelGGL((decode_split<DT, ND, true>), dim3(W), dim3(256), 0, L.stream, A);
   else
@@ -469,8 +562,7 @@ int go(const Launch &L, const DecodeArgs &A, int64_t units, bool splits) {
 }  // namespace
 
 size_t attn_decode_workspace_bytes(int R, int batch, int64_t max_len, int heads, int kv_heads, int D) {
-  const int64_t units = unit_bound(R, batch, max_len, heads, kv_heads);
-  const size_t W = (size_t)split_of(units);
+  const size_t W = (size_t)split_of(unit_bound(R, batch, max_len), wide_of(heads, kv_heads));
   const size_t slot = (size_t)(kHeadTile * D + 2 * kHeadTile) * sizeof(float);
   return (W * sizeof(int4) + 255) / 256 * 256 + (2 * W * slot + 255) / 256 * 256;
 }
@@ -482,7 +574,7 @@ int launch_attn_decode(const Launch &L, int R, const PtrTable &q, const PtrTable
                        int kv_heads, int D, int64_t q_stride, int64_t o_stride, int64_t page_stride,
                        int64_t tok_stride, int64_t head_stride, float scale, int dt, void *ws) {
   const int64_t max_len = (int64_t)max_pages * page_size;
-  const int64_t units = unit_bound(R, batch, max_len, heads, kv_heads);
+  const int64_t units = unit_bound(R, batch, max_len), wide = wide_of(heads, kv_heads);
   if (units >= (1ll << 31) || max_len > (1ll << 31) - 8 * kUnit) return COLL_ERR_UNSUPPORTED;
   DecodeArgs A{};
   A.q = q, A.k = k, A.v = v, A.table = table, A.lens = lens, A.seqs = seqs, A.o = o, A.lse = lse;
@@ -498,17 +590,19 @@ int launch_attn_decode(const Launch &L, int R, const PtrTable &q, const PtrTable
   A.by_head_tiles = make_fastdiv((uint32_t)A.head_tiles);
   A.negate = scale < 0.0f;
   A.c = __builtin_fabsf(scale) * kLog2e;
-  const size_t W = (size_t)split_of(units);
+  A.heads_wide = (int)wide;
+  A.by_wide = make_fastdiv((uint32_t)wide);
+  const size_t W = (size_t)split_of(units, wide);
   A.joins = reinterpret_cast<int4 *>(ws);
   A.part = reinterpret_cast<float *>(reinterpret_cast<char *>(ws) + (W * sizeof(int4) + 255) / 256 * 256);
   const bool splits = max_len > kUnit;
 #define COLL_DECODE(DTV)                                   \
   switch (D) {                                             \
-    case 64: return go<DTV, 2>(L, A, units, splits);       \
-    case 96: return go<DTV, 3>(L, A, units, splits);       \
-    case 128: return go<DTV, 4>(L, A, units, splits);      \
-    case 192: return go<DTV, 6>(L, A, units, splits);      \
-    case 256: return go<DTV, 8>(L, A, units, splits);      \
+    case 64: return go<DTV, 2>(L, A, (int)W, splits);       \
+    case 96: return go<DTV, 3>(L, A, (int)W, splits);       \
+    case 128: return go<DTV, 4>(L, A, (int)W, splits);      \
+    case 192: return go<DTV, 6>(L, A, (int)W, splits);      \
+    case 256: return go<DTV, 8>(L, A, (int)W, splits);      \
     default: return COLL_ERR_UNSUPPORTED;                  \
   }
   if (dt == COLL_BF16) { COLL_DECODE(COLL_BF16) }

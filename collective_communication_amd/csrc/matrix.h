@@ -52,6 +52,14 @@ __device__ __forceinline__ u32x2 lds_tr16(const void *p) {
 __device__ __forceinline__ float exp2_f(float x) { return __builtin_amdgcn_exp2f(x); }
 __device__ __forceinline__ float log2_f(float x) { return __builtin_amdgcn_logf(x); }
 
+// Between LDS writes of a wave and its reads of what other lanes of the same
+// wave wrote (or the other way round): the hardware keeps a wave's LDS
+// accesses in order, so only the compiler has to.
+__device__ __forceinline__ void wave_lds_sync() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+}
+
 // max over lanes l and l ^ 32
 __device__ __forceinline__ float max_halves(float x) {
   const uint32_t b = __builtin_bit_cast(uint32_t, x);

@@ -63,31 +63,33 @@ __device__ __forceinline__ i32x4 refs4(const PageState &S, int i) {
 
 // Allocation for extend and fork.  Entry i (lane i) wants need pages; served
 // are the entries whose running total, in list order, fits the free pages.
-// give(k, page) is called once for each of the first `served` pages.
+// The first 4096 refs are read once, by the caller, before anything depends
+// on them.
 struct Demand {
   int upto;       // running total up to and including the entry
   int free;       // free pages
 };
-__device__ __forceinline__ Demand demand(const PageState &S, int need, int *s_wave) {
+__device__ __forceinline__ int zeros(i32x4 x) {
+  return (x[0] == 0) + (x[1] == 0) + (x[2] == 0) + (x[3] == 0);
+}
+__device__ __forceinline__ Demand demand(const PageState &S, i32x4 refs0, int need, int *s_wave) {
   Demand d;
   int total;
   d.upto = scan_block(need, s_wave, &total);
-  int n = 0;
-  for (int i = 4 * (int)threadIdx.x; i < S.num_pages; i += 4 * kOne) {
-    const i32x4 x = refs4(S, i);
-#pragma unroll
-    for (int j = 0; j < 4; j++) n += x[j] == 0;
-  }
+  int n = zeros(refs0);
+  for (int i = 4 * (kOne + (int)threadIdx.x); i < S.num_pages; i += 4 * kOne) n += zeros(refs4(S, i));
   scan_block(n, s_wave, &d.free);
   return d;
 }
+// give(k, page) for the k-th free page, k < want
 template <class Give>
-__device__ __forceinline__ void take_free(const PageState &S, int want, int *s_wave, Give give) {
+__device__ __forceinline__ void take_free(const PageState &S, i32x4 refs0, int want, int *s_wave,
+                                          Give give) {
   int done = 0;
   for (int base = 0; base < S.num_pages && done < want; base += 4 * kOne) {
     const int i = base + 4 * (int)threadIdx.x;
-    const i32x4 x = refs4(S, i);
-    const int mine = (x[0] == 0) + (x[1] == 0) + (x[2] == 0) + (x[3] == 0);
+    const i32x4 x = base == 0 ? refs0 : refs4(S, i);
+    const int mine = zeros(x);
     int total;
     int k = done + scan_block(mine, s_wave, &total) - mine;
 #pragma unroll
@@ -111,41 +113,63 @@ __device__ __forceinline__ int owner_of(const int *upto, int n, int k) {
   return lo;
 }
 
-// Whether an entry before i names the same row.
-__device__ __forceinline__ bool named_before(const int *rows, int i) {
-  bool seen = false;
-  for (int j = 0; j < i; j++) seen = seen || rows[j] == rows[i];
-  return seen;
+// The first entry that names each row, in an LDS hash of twice the entries'
+// number (open addressing; an entry's probe ends at its row or a free place,
+// and there always is one).
+constexpr int kHash = 2 * kOne;
+struct RowHash {
+  int row[kHash], first[kHash];
+};
+__device__ __forceinline__ void hash_clear(RowHash &T) {
+  for (int x = threadIdx.x; x < kHash; x += kOne) {
+    T.row[x] = -1;
+    T.first[x] = kOne;
+  }
 }
+__device__ __forceinline__ int hash_add(RowHash &T, int row, int i) {     // row >= 0
+  int x = (int)(((uint32_t)row * 2654435761u) >> 21);
+  for (;;) {
+    const int had = atomicCAS(&T.row[x], -1, row);
+    if (had == -1 || had == row) break;
+    x = (x + 1) & (kHash - 1);
+  }
+  atomicMin(&T.first[x], i);
+  return x;
+}
+static_assert(kHash == 1 << (32 - 21), "the hash takes the top bits");
 
 __global__ __launch_bounds__(kOne) void extend_rows(PageState S, const int32_t *seqs,
                                                     const int32_t *add, int n, int32_t *status) {
   __shared__ int s_wave[kOneWaves], s_row[kOne], s_upto[kOne], s_have[kOne];
+  __shared__ RowHash s_hash;
   __shared__ int s_want;
   const int i = threadIdx.x;
-  const int row = i < n ? seqs[i] : -1;
+  const int row = i < n ? seqs[i] : -1, more = i < n ? add[i] : 0;
+  const i32x4 refs0 = refs4(S, 4 * i);
   s_row[i] = row;
+  hash_clear(s_hash);
   if (i == 0) s_want = 0;
   __syncthreads();
-  bool ok = i < n && row >= 0 && row < S.rows && !named_before(s_row, i);
-  int len = 0, more = 0, have = 0, need = 0;
+  bool ok = i < n && row >= 0 && row < S.rows;
+  int len = 0, have = 0, need = 0;
+  if (ok) len = S.lens[row];
+  const int place = ok ? hash_add(s_hash, row, i) : 0;
+  __syncthreads();
   if (ok) {
-    len = S.lens[row];
-    more = add[i];
-    ok = len >= 0 && more >= 0 && (int64_t)len + more <= (int64_t)S.width * S.page_size;
+    ok = s_hash.first[place] == i && len >= 0 && more >= 0 && (int64_t)len + more <= (int64_t)S.width * S.page_size;
   }
   if (ok) {
     have = pages_of(S, len);
     need = pages_of(S, len + more) - have;
   }
-  const Demand d = demand(S, need, s_wave);
+  const Demand d = demand(S, refs0, need, s_wave);
   const bool served = ok && d.upto <= d.free;
   s_upto[i] = d.upto;
   s_have[i] = have;
   // the pages of the last served entry end the list
   if (served && need > 0) atomicMax(&s_want, d.upto);
   __syncthreads();
-  take_free(S, s_want, s_wave, [&](int k, int page) {
+  take_free(S, refs0, s_want, s_wave, [&](int k, int page) {
     const int e = owner_of(s_upto, kOne, k);
     const int at = s_have[e] + k - (e ? s_upto[e - 1] : 0);
     S.table[(int64_t)s_row[e] * S.width + at] = page;
@@ -159,37 +183,63 @@ __global__ __launch_bounds__(kOne) void extend_rows(PageState S, const int32_t *
 
 // Fork, first kernel: which entries are served, a fresh page and a copy for
 // each partly filled one, and the destinations' lengths.  Every length is
-// read before any is written.  The rows follow in fork_rows.
+// read before any is written.  Few rows (kForkInline table entries) are
+// shared here too, more of them in fork_rows (free, fork and copy of 4 forks of
+// 20 columns: 14.8 us against 18.5 with the second kernel; of 128 forks of 45
+// columns: 42.7 against 39).
+constexpr int kForkInline = 4 * kOne;
+// Column c of a destination's row: the source's page, shared, below `full`, the
+// fresh page (written by fork_plan) up to `used`, none behind it.
+__device__ __forceinline__ void share_page(const PageState &S, int from, int to, int c, int full,
+                                           int used) {
+  int32_t *d = S.table + (int64_t)to * S.width + c;
+  if (c < full) {
+    const int32_t p = S.table[(int64_t)from * S.width + c];
+    *d = p;
+    if (p >= 0 && p < S.num_pages) atomicAdd(&S.ref[p], 1);
+  } else if (c >= used) {
+    *d = -1;
+  }
+}
 __global__ __launch_bounds__(kOne) void fork_plan(PageState S, const int32_t *src,
                                                   const int32_t *dst, int n, int32_t *moves,
-                                                  int32_t *count, int32_t *status) {
+                                                  int32_t *count, int32_t *status, int inline_rows,
+                                                  FastDiv by_width) {
   __shared__ int s_wave[kOneWaves], s_row[kOne], s_upto[kOne], s_src[kOne], s_full[kOne];
+  __shared__ int s_used[kOne];
+  __shared__ RowHash s_hash;
   __shared__ int s_want;
   const int i = threadIdx.x;
   const int from = i < n ? src[i] : -1, to = i < n ? dst[i] : -1;
+  const i32x4 refs0 = refs4(S, 4 * i);
   s_row[i] = to;
   s_src[i] = from;
+  hash_clear(s_hash);
   if (i == 0) s_want = 0;
   __syncthreads();
-  bool ok = i < n && from >= 0 && from < S.rows && to >= 0 && to < S.rows && from != to &&
-            !named_before(s_row, i);
-  int len = 0, full = 0, need = 0;
+  bool ok = i < n && from >= 0 && from < S.rows && to >= 0 && to < S.rows && from != to;
+  const bool named = i < n && to >= 0;
+  int len = 0, had = 0, full = 0, need = 0;
   if (ok) {
     len = S.lens[from];
-    ok = len >= 0 && len <= (int64_t)S.width * S.page_size && S.lens[to] == 0;
+    had = S.lens[to];
   }
+  const int place = named ? hash_add(s_hash, to, i) : 0;
+  __syncthreads();
+  ok = ok && s_hash.first[place] == i && len >= 0 && len <= (int64_t)S.width * S.page_size && had == 0;
   if (ok) {
     full = (int)fdiv((uint32_t)len, S.by_page);
     need = len - full * S.page_size > 0;
   }
-  const Demand d = demand(S, need, s_wave);
+  const Demand d = demand(S, refs0, need, s_wave);
   const bool served = ok && d.upto <= d.free;
   s_upto[i] = d.upto;
   s_full[i] = full;
+  s_used[i] = served ? full + need : -1;
   if (served && need > 0) atomicMax(&s_want, d.upto);
   __syncthreads();
   const int want = s_want;
-  take_free(S, want, s_wave, [&](int k, int page) {
+  take_free(S, refs0, want, s_wave, [&](int k, int page) {
     const int e = owner_of(s_upto, kOne, k);
     const int old = S.table[(int64_t)s_src[e] * S.width + s_full[e]];
     S.table[(int64_t)s_row[e] * S.width + s_full[e]] = page;
@@ -206,6 +256,11 @@ __global__ __launch_bounds__(kOne) void fork_plan(PageState S, const int32_t *sr
     if (served) S.lens[to] = len;
     status[i] = served ? 0 : (ok ? -2 : -1);
   }
+  if (inline_rows)
+    for (int x = i; x < n * S.width; x += kOne) {
+      const int e = (int)fdiv((uint32_t)x, by_width);
+      if (s_used[e] >= 0) share_page(S, s_src[e], s_row[e], x - e * S.width, s_full[e], s_used[e]);
+    }
 }
 
 // Fork, second kernel: one workgroup per entry shares the source's whole
@@ -219,17 +274,7 @@ __global__ __launch_bounds__(kBlock) void fork_rows(PageState S, const int32_t *
   const int from = src[i], to = dst[i];
   const int len = S.lens[to], full = (int)fdiv((uint32_t)len, S.by_page);
   const int used = full + (len > full * S.page_size);
-  const int32_t *a = S.table + (int64_t)from * S.width;
-  int32_t *b = S.table + (int64_t)to * S.width;
-  for (int c = threadIdx.x; c < S.width; c += kBlock) {
-    if (c < full) {
-      const int32_t p = a[c];
-      b[c] = p;
-      if (p >= 0 && p < S.num_pages) atomicAdd(&S.ref[p], 1);
-    } else if (c >= used) {
-      b[c] = -1;
-    }
-  }
+  for (int c = threadIdx.x; c < S.width; c += kBlock) share_page(S, from, to, c, full, used);
 }
 
 __global__ __launch_bounds__(kBlock) void free_rows(PageState S, const int32_t *seqs) {
@@ -319,35 +364,41 @@ __global__ __launch_bounds__(kBlock) void compact_table(PageState S, const int32
   if (p >= 0 && p < S.num_pages) S.table[i] = map[p];
 }
 
-// Copies pages moves[m] = (from, to) of every pool and layer, m < *count.
-// One workgroup per tile of a page; the grid covers a resident set of tiles
-// and loops, since only the device knows the count.
-constexpr int kCopyTile = 1024;          // units of a tile: 4 per lane
+// Copies pages moves[m] = (from, to) of every pool and layer, m < *count.  The
+// grid is resident and loops over 16 KiB tiles, since only the device knows
+// the count; all moves of one pool and layer come before the next, so that
+// what is in flight lies within one region (1 GB of traffic over 2 pools of
+// 8 layers: 191-195 us against 206 with the pools and layers of a move first;
+// 2, 3, 4 and 8 workgroups a compute unit: 191, 195, 198, 201; plain instead of
+// non-temporal accesses: 208).
+constexpr int kCopyPer = 4, kCopyTile = kCopyPer * kBlock;     // units of a lane and of a tile
+constexpr unsigned kCopyGrid = 3;                              // workgroups a compute unit
 template <int B, bool NT>
-__global__ __launch_bounds__(kBlock) void copy_pages(MutPtrTable pools, int npools, uint64_t layers,
+__global__ __launch_bounds__(kBlock) void copy_pages(MutPtrTable pools, FastDiv by_pools,
+                                                     FastDiv by_tiles, uint32_t regions,
                                                      uint64_t num_pages, uint64_t page_units,
                                                      const int32_t *moves, int max_moves,
-                                                     const int32_t *count, uint32_t tiles) {
+                                                     const int32_t *count) {
   typedef typename UnitT<B>::T U;
-  int n = count ? *count : max_moves;
-  n = n < 0 ? 0 : (n < max_moves ? n : max_moves);
-  const uint64_t per = (uint64_t)npools * layers * tiles, total = per * (uint64_t)n;
-  for (uint64_t x = blockIdx.x; x < total; x += gridDim.x) {
-    const uint64_t m = x / per, y = x - m * per;
-    const uint32_t tile = (uint32_t)(y % tiles);
-    const uint64_t z = y / tiles, pool = z % npools, layer = z / npools;
-    const int64_t a = moves[2 * m], b = moves[2 * m + 1];
+  int c = count ? *count : max_moves;
+  const uint32_t n = c < 0 ? 0 : (uint32_t)(c < max_moves ? c : max_moves);
+  const uint32_t total = regions * by_tiles.d * n;               // < 2^31 - the grid
+  for (uint32_t x = blockIdx.x; x < total; x += gridDim.x) {
+    const uint32_t q = fdiv(x, by_tiles), tile = x - q * by_tiles.d;
+    const uint32_t z = q / n, m = q - z * n;
+    const uint32_t layer = fdiv(z, by_pools), pool = z - layer * by_pools.d;
+    const int64_t a = moves[2 * (size_t)m], b = moves[2 * (size_t)m + 1];
     if (a < 0 || b < 0 || (uint64_t)a >= num_pages || (uint64_t)b >= num_pages || a == b) continue;
     char *base = reinterpret_cast<char *>(pools.p[pool]) + layer * num_pages * page_units * B;
     const U *s = reinterpret_cast<const U *>(base) + (uint64_t)a * page_units;
     U *d = reinterpret_cast<U *>(base) + (uint64_t)b * page_units;
     const uint64_t at = (uint64_t)tile * kCopyTile + threadIdx.x;
-    U v[4];
+    U v[kCopyPer];
 #pragma unroll
-    for (int j = 0; j < 4; j++)
+    for (int j = 0; j < kCopyPer; j++)
       if (at + j * kBlock < page_units) v[j] = ld<U, NT>(s, at + j * kBlock);
 #pragma unroll
-    for (int j = 0; j < 4; j++)
+    for (int j = 0; j < kCopyPer; j++)
       if (at + j * kBlock < page_units) st<U, NT>(d, at + j * kBlock, v[j]);
   }
 }
@@ -363,20 +414,33 @@ struct WriteArgs {
   FastDiv by_page, by_head, by_tokens;
 };
 
-// New tokens' keys and values: a wave per (rank, token) copies both rows.
+// New tokens' keys and values: a wave per (rank, token) copies both rows.  It
+// loads up to 2 KiB of each before it looks up where they go.
+constexpr int kWriteAhead = 2;           // units of a lane loaded ahead, of each row
 __global__ __launch_bounds__(kBlock) void write_rows(WriteArgs A, uint32_t waves) {
   const uint32_t w = blockIdx.x * (kBlock / 64) + (threadIdx.x >> 6);
   if (w >= waves) return;
-  const int lane = threadIdx.x & 63;
+  const uint32_t lane = threadIdx.x & 63;
   const uint32_t r = fdiv(w, A.by_tokens);
   const int64_t t = w - r * (uint32_t)A.tokens;
+  const char *ks = reinterpret_cast<const char *>(A.k.p[r]) + t * A.k_stride * 2;
+  const char *vs = reinterpret_cast<const char *>(A.v.p[r]) + t * A.v_stride * 2;
+  u32x4 kx[kWriteAhead], vx[kWriteAhead];
+#pragma unroll
+  for (int j = 0; j < kWriteAhead; j++)
+    if (lane + 64 * j < A.row_units) {
+      kx[j] = ld<u32x4>(ks, lane + 64 * j);
+      vx[j] = ld<u32x4>(vs, lane + 64 * j);
+    }
+  // the last b with starts[b] <= t, 64 ways at a time
   const int32_t *starts = reinterpret_cast<const int32_t *>(A.starts.p[r]);
-  // the last b with starts[b] <= t
-  int lo = 0, hi = A.batch;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (starts[mid] <= t) lo = mid;
-    else hi = mid;
+  int lo = 0, n = A.batch;
+  while (n > 1) {
+    const int step = (n + 63) >> 6, i = (int)lane * step;
+    const uint64_t below = __ballot(i < n && starts[lo + i] <= t);
+    const int c = below ? 63 - __builtin_clzll(below) : 0;
+    lo += c * step;
+    n = n - c * step < step ? n - c * step : step;
   }
   const int64_t a = starts[lo], z = starts[lo + 1];
   if (a < 0 || t < a || t >= z) return;
@@ -389,16 +453,18 @@ __global__ __launch_bounds__(kBlock) void write_rows(WriteArgs A, uint32_t waves
   const int64_t page = reinterpret_cast<const int32_t *>(A.table.p[r])[(int64_t)row * A.max_pages + pi];
   if (page < 0 || page >= A.num_pages) return;
   const int64_t to = page * A.page_stride + slot * A.tok_stride;
-  const char *ks = reinterpret_cast<const char *>(A.k.p[r]) + t * A.k_stride * 2;
-  const char *vs = reinterpret_cast<const char *>(A.v.p[r]) + t * A.v_stride * 2;
   char *kd = reinterpret_cast<char *>(A.kp.p[r]), *vd = reinterpret_cast<char *>(A.vp.p[r]);
-  for (uint32_t u = lane; u < A.row_units; u += 64) {
+  auto put = [&](uint32_t u, u32x4 x, u32x4 y) {
     const uint32_t h = fdiv(u, A.by_head);
     const int64_t off = (to + h * A.head_stride) * 2 + (u - h * A.head_units) * 16;
-    const u32x4 x = ld<u32x4>(ks, u), y = ld<u32x4>(vs, u);
     *reinterpret_cast<u32x4 *>(kd + off) = x;
     *reinterpret_cast<u32x4 *>(vd + off) = y;
-  }
+  };
+#pragma unroll
+  for (int j = 0; j < kWriteAhead; j++)
+    if (lane + 64 * j < A.row_units) put(lane + 64 * j, kx[j], vx[j]);
+  for (uint32_t u = lane + 64 * kWriteAhead; u < A.row_units; u += 64)
+    put(u, ld<u32x4>(ks, u), ld<u32x4>(vs, u));
 }
 
 PageState state(int32_t *table, int32_t *lens, int32_t *ref, int rows, int width, int num_pages,
@@ -424,10 +490,12 @@ int launch_kv_fork(const Launch &L, int32_t *table, int32_t *lens, int32_t *ref,
                    int width, int num_pages, int page_size, const int32_t *src,
                    const int32_t *dst, int n, int32_t *moves, int32_t *count, int32_t *status) {
   const PageState S = state(table, lens, ref, rows, width, num_pages, page_size);
+  const bool few = (int64_t)n * width <= kForkInline;
   hipLaunchKernelGGL(fork_plan, dim3(1), dim3(kOne), 0, L.stream, S, src, dst, n, moves, count,
-                     status);
-  hipLaunchKernelGGL(fork_rows, dim3(n), dim3(kBlock), 0, L.stream, S, src, dst,
-                     (const int32_t *)status);
+                     status, (int)few, make_fastdiv((uint32_t)(width > 0 ? width : 1)));
+  if (!few)
+    hipLaunchKernelGGL(fork_rows, dim3(n), dim3(kBlock), 0, L.stream, S, src, dst,
+                       (const int32_t *)status);
   return hip_status();
 }
 
@@ -461,13 +529,17 @@ int launch_kv_copy_pages(const Launch &L, int npools, const MutPtrTable &pools, 
   const int unit = copy_unit(bits);
   const uint64_t units = page_bytes / unit;
   const uint64_t tiles = (units + kCopyTile - 1) / kCopyTile;
-  if (tiles > 0xFFFFFFFFull) return COLL_ERR_UNSUPPORTED;
-  const uint64_t most = (uint64_t)npools * layers * tiles * (uint64_t)max_moves;
-  const uint64_t resident = (uint64_t)L.num_cus * 8;
+  const uint64_t resident = (uint64_t)L.num_cus * kCopyGrid, lim = (1ull << 31) - resident;
+  const uint64_t regions = (uint64_t)npools * layers;
+  if (layers >= lim || tiles >= lim || regions >= lim / tiles ||
+      (uint64_t)max_moves >= lim / (regions * tiles))
+    return COLL_ERR_UNSUPPORTED;
+  const uint64_t most = regions * tiles * (uint64_t)max_moves;
   const unsigned grid = (unsigned)(most < resident ? most : resident);
-  const bool nt = false;
-  COLL_UNIT_SWITCH(copy_pages, unit, nt, dim3(grid), L.stream, pools, npools, (uint64_t)layers,
-                   (uint64_t)num_pages, units, moves, max_moves, count, (uint32_t)tiles);
+  const bool nt = 2 * regions * page_bytes * (uint64_t)max_moves >= L.nt_bytes;
+  COLL_UNIT_SWITCH(copy_pages, unit, nt, dim3(grid), L.stream, pools, make_fastdiv((uint32_t)npools),
+                   make_fastdiv((uint32_t)tiles), (uint32_t)regions, (uint64_t)num_pages, units, moves,
+                   max_moves, count);
   return hip_status();
 }
 

@@ -196,6 +196,11 @@ def fam_decode():
     decode_case("ragged ranks", 2, 4, 2, 64, [300, 0, 1, 129, 128, 40], 32, dtype="fp16")
     for D, dtype in ((64, "bf16"), (96, "fp16"), (128, "fp16"), (192, "bf16"), (256, "fp16")):
         decode_case("dims", 1, 3, 3, D, [200, 37], 8, dtype=dtype, seed=D)
+        decode_case("dims, split", 2, 3, 3, D, [200, 37, 700], 8, dtype=dtype, seed=D, width=130)
+    decode_case("ragged ranks, split", 2, 4, 2, 64, [300, 0, 1, 129, 128, 40], 32, dtype="fp16", width=40)
+    decode_case("20 heads share, split", 1, 40, 2, 64, [640, 260], 16, width=70)
+    decode_case("pages of 3, split", 1, 2, 1, 128, [650, 3], 3, width=400)
+    decode_case("300 entries, split", 2, 1, 1, 64, [1 + (7 * i) % 300 for i in range(300)], 32, width=40)
     decode_case("pages of 20", 1, 4, 2, 128, [333, 19, 20, 21], 20)
     decode_case("pages of 1", 1, 2, 1, 64, [150], 1)
     decode_case("pages of 3, D 256", 1, 2, 1, 256, [150], 3)
@@ -362,6 +367,8 @@ def fam_pages():
     state_case("1024 entries", 1100, 1, 2, 5000, [1] * 40,
                [("extend", list(range(1024)), [i % 3 for i in range(1024)]), ("free", list(range(0, 1024))),
                 ("compact",)])
+    state_case("rows of a wide table", 60, 700, 4, 700, [30, 2500],
+               [("fork", [0, 1, 0] * 10, list(range(5, 35))), ("compact",), ("free", [1, 6])])
     state_case("nothing free", 3, 4, 2, 4, [8], [("extend", [1], [1]), ("compact",), ("fork", [0], [2])])
     state_case("nothing used", 3, 4, 2, 9, [], [("compact",), ("free", [0, 1])])
     copy_case("one", 1, 1, 4, 64, [(0, 2)])

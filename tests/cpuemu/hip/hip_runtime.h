@@ -204,6 +204,10 @@ static inline float max_halves(float x, const char *f = __builtin_FILE(), int l 
   const int other = (int)(emu_thread_idx()->x & 63) ^ 32;
   return fmaxf(x, emu_shfl_at(x, other, 64, f, l));
 }
+// every lane of the wave gets here before any goes on
+static inline void wave_lds_sync(const char *f = __builtin_FILE(), int l = __builtin_LINE()) {
+  (void)emu_wave_op(EMU_BALLOT, 1, 0, f, l);
+}
 struct int4 {
   int x, y, z, w;
 };
@@ -228,6 +232,18 @@ template <class T>
 static inline T atomicMax(T *p, T v) {
   T old = *p;
   if (v > old) *p = v;
+  return old;
+}
+template <class T>
+static inline T atomicMin(T *p, T v) {
+  T old = *p;
+  if (v < old) *p = v;
+  return old;
+}
+template <class T>
+static inline T atomicCAS(T *p, T expected, T v) {
+  T old = *p;
+  if (old == expected) *p = v;
   return old;
 }
 
