@@ -167,36 +167,29 @@ __global__ __launch_bounds__(NW * 64, COLL_PROMPT_OCC) void prompt_tiles(PromptA
   }
 
   // a thread's chunks of a tile: key kr0[i] of the tile, 16 bytes at chunk c
-  u32x4 rk[NCH], rv[NCH];
+  u32x4 held[NCH];
   const char *kp = reinterpret_cast<const char *>(A.k.p[r]) + (t.k0 * A.k_stride + (int64_t)kvh * D) * 2;
   const char *vp = reinterpret_cast<const char *>(A.v.p[r]) + (t.k0 * A.v_stride + (int64_t)kvh * D) * 2;
-  auto load_one = [&](u32x4 (&dst)[NCH], const char *src, int64_t stride, int kt) {
+  auto load = [&](const char *src, int64_t stride, int kt) {
 #pragma unroll
     for (int i = 0; i < NCH; i++) {
       const int x = tid + i * NT, kr = x / CH, c = x - kr * CH;
       const int key = kt * BN + kr;
       u32x4 a = {0, 0, 0, 0};
       if ((kWhole || x < BN * CH) && key < t.nk) a = ld<u32x4>(src + key * stride * 2, c);
-      dst[i] = a;
+      held[i] = a;
     }
   };
-  auto load_k = [&](int kt) { load_one(rk, kp, A.k_stride, kt); };
-  auto load_v = [&](int kt) { load_one(rv, vp, A.v_stride, kt); };
-  auto store_k = [&](int kt) {
+  auto store = [&](uint16_t *tile, int row) {
 #pragma unroll
     for (int i = 0; i < NCH; i++) {
       const int x = tid + i * NT, kr = x / CH, c = x - kr * CH;
-      if (kWhole || x < BN * CH)
-        *reinterpret_cast<u32x4 *>(s_t.k[kt & 1] + kr * TL::kRowK + 8 * c) = rk[i];
+      if (kWhole || x < BN * CH) *reinterpret_cast<u32x4 *>(tile + kr * row + 8 * c) = held[i];
     }
   };
+  auto store_k = [&](int kt) { store(s_t.k[kt & 1], TL::kRowK); };
   auto store_v = [&](int kt) {
-#pragma unroll
-    for (int i = 0; i < NCH; i++) {
-      const int x = tid + i * NT, kr = x / CH, c = x - kr * CH;
-      if (kWhole || x < BN * CH)
-        *reinterpret_cast<u32x4 *>(s_t.v[kt & 1] + kr * TL::kRowV + 8 * c) = rv[i];
-    }
+    store(s_t.v[kt & 1], TL::kRowV);
     // a value that is not finite at a key some row must not see would reach
     // that row as 0 * inf: such a tile is marked for the careful product
     if ((kt + 1) * BN > see_all) {
@@ -204,7 +197,7 @@ __global__ __launch_bounds__(NW * 64, COLL_PROMPT_OCC) void prompt_tiles(PromptA
 #pragma unroll
       for (int i = 0; i < NCH; i++)
 #pragma unroll
-        for (int e = 0; e < 4; e++) bad = bad || pair_not_finite<DT>(rv[i][e]);
+        for (int e = 0; e < 4; e++) bad = bad || pair_not_finite<DT>(held[i][e]);
       if (bad) s_bad[kt & 1] = kt + 1;
     }
   };
@@ -218,19 +211,16 @@ __global__ __launch_bounds__(NW * 64, COLL_PROMPT_OCC) void prompt_tiles(PromptA
   // part of the sum, in two
   float m = -__builtin_inff(), l0 = 0.0f, l1 = 0.0f;
 
-  // S^T of a tile, 32 keys per accumulator
+  // S^T of 32 keys of a tile
   const int kat = col * TL::kRowK + 8 * g;
-  auto scores = [&](int kt, f32x16 (&s)[KT]) {
-    const uint16_t *base = s_t.k[kt & 1] + kat;
+  auto scores = [&](int kt, int half) -> f32x16 {
+    const uint16_t *base = s_t.k[kt & 1] + kat + 32 * half * TL::kRowK;
+    f32x16 s;
 #pragma unroll
-    for (int x = 0; x < KT; x++)
+    for (int e = 0; e < 16; e++) s[e] = 0.0f;
 #pragma unroll
-      for (int e = 0; e < 16; e++) s[x][e] = 0.0f;
-#pragma unroll
-    for (int d = 0; d < DK; d++)
-#pragma unroll
-      for (int x = 0; x < KT; x++)
-        s[x] = mma32<DT>(*reinterpret_cast<const u32x4 *>(base + x * 32 * TL::kRowK + 16 * d), q[d], s[x]);
+    for (int d = 0; d < DK; d++) s = mma32<DT>(*reinterpret_cast<const u32x4 *>(base + 16 * d), q[d], s);
+    return s;
   };
   // V^T as the A operand of rows 32 d.., keys 16 s ..: two transposing reads,
   // keys 16 s + 4 g + 0..3 and those 8 further on
@@ -265,35 +255,32 @@ __global__ __launch_bounds__(NW * 64, COLL_PROMPT_OCC) void prompt_tiles(PromptA
         for (int e = 0; e < 16; e++) acc[d][e] *= f;
     }
   };
-  auto weights = [&](const f32x16 (&s)[KT], u32x4 (&p)[BN / 16]) {
+  // the weights of 32 keys, as the B operands of two products of 16
+  auto weights = [&](const f32x16 &s, u32x4 (&p)[2]) {
     const float mc = m == -__builtin_inff() ? 0.0f : m * A.c;
 #pragma unroll
-    for (int x = 0; x < KT; x++)
-#pragma unroll
-      for (int e = 0; e < 16; e += 2) {
-        const float y0 = exp2_f(__builtin_fmaf(s[x][e], A.c, -mc));
-        const float y1 = exp2_f(__builtin_fmaf(s[x][e + 1], A.c, -mc));
-        l0 += y0;
-        l1 += y1;
-        p[2 * x + (e >> 3)][(e & 7) >> 1] = pack2<DT>(y0, y1);
-      }
+    for (int e = 0; e < 16; e += 2) {
+      const float y0 = exp2_f(__builtin_fmaf(s[e], A.c, -mc));
+      const float y1 = exp2_f(__builtin_fmaf(s[e + 1], A.c, -mc));
+      l0 += y0;
+      l1 += y1;
+      p[e >> 3][(e & 7) >> 1] = pack2<DT>(y0, y1);
+    }
   };
 
   const int ntiles = (n_block + BN - 1) / BN;
   const int nfull = see_all / BN < ntiles ? see_all / BN : ntiles;   // tiles that need no mask
   if (tid < 2) s_bad[tid] = 0;
-  if (ntiles > 0) {
-    load_k(0);
-    load_v(0);
-  }
   __syncthreads();
   if (ntiles > 0) {
+    load(kp, A.k_stride, 0);
     store_k(0);
+    load(vp, A.v_stride, 0);
     store_v(0);
-    if (ntiles > 1) {
-      load_k(1);
-      store_k(1);
-    }
+  }
+  if (ntiles > 1) {
+    load(kp, A.k_stride, 1);
+    store_k(1);
   }
   __syncthreads();
 
@@ -303,80 +290,95 @@ __global__ __launch_bounds__(NW * 64, COLL_PROMPT_OCC) void prompt_tiles(PromptA
   // last read before the previous one.
   f32x16 s[KT];
   const bool busy = n_wave > 0;
-  if (busy) scores(0, s);
+  if (busy)
+#pragma unroll
+    for (int x = 0; x < KT; x++) s[x] = scores(0, x);
   __syncthreads();
   int kt = 0;
   for (; kt < nfull; kt++) {
-    if (kt + 2 < ntiles) load_k(kt + 2);
-    if (kt + 1 < ntiles) load_v(kt + 1);
+    // K's tile passes through the staging registers in the first half, V's in
+    // the last
+    const bool more_k = kt + 2 < ntiles, more_v = kt + 1 < ntiles;
+    if (more_k) load(kp, A.k_stride, kt + 2);
     if (busy) {
       raise(s);
-      u32x4 p[BN / 16];
       f32x16 nx[KT];
-      weights(s, p);
-      scores(kt + 1, nx);                             // of an old tile after the last one: not used
 #pragma unroll
-      for (int x = 0; x < BN / 16; x++)
+      for (int x = 0; x < KT; x++) {
+        if (x == KT - 1) {
+          if (more_k) store_k(kt + 2);
+          if (more_v) load(vp, A.v_stride, kt + 1);
+        }
+        u32x4 p[2];
+        weights(s[x], p);
+        nx[x] = scores(kt + 1, x);                    // of an old tile after the last one: not used
 #pragma unroll
-        for (int d = 0; d < DV; d++) acc[d] = mma32<DT>(v_frag(kt, d, x), p[x], acc[d]);
+        for (int y = 0; y < 2; y++)
+#pragma unroll
+          for (int d = 0; d < DV; d++) acc[d] = mma32<DT>(v_frag(kt, d, 2 * x + y), p[y], acc[d]);
+      }
 #pragma unroll
       for (int x = 0; x < KT; x++) s[x] = nx[x];
+    } else {
+      if (more_k) store_k(kt + 2);
+      if (more_v) load(vp, A.v_stride, kt + 1);
     }
-    if (kt + 2 < ntiles) store_k(kt + 2);
-    if (kt + 1 < ntiles) store_v(kt + 1);
+    if (more_v) store_v(kt + 1);
     __syncthreads();
   }
   for (; kt < ntiles; kt++) {                         // tiles on the diagonal and the last one
-    if (kt + 2 < ntiles) load_k(kt + 2);
-    if (kt + 1 < ntiles) load_v(kt + 1);
-    const int key0 = kt * BN;
-    if (key0 < n_wave) {
+    if (kt + 2 < ntiles) {
+      load(kp, A.k_stride, kt + 2);
+      store_k(kt + 2);
+    }
+    if (kt + 1 < ntiles) load(vp, A.v_stride, kt + 1);
+    if (kt * BN < n_wave) {
 #pragma unroll
       for (int x = 0; x < KT; x++)
 #pragma unroll
-        for (int e = 0; e < 16; e++) {
-          const int key = key0 + 32 * x + (e & 3) + 8 * (e >> 2) + 4 * g;
-          s[x][e] = key < lim ? s[x][e] : -__builtin_inff();
-        }
+        for (int e = 0; e < 16; e++)
+          s[x][e] = kt * BN + 32 * x + (e & 3) + 8 * (e >> 2) + 4 * g < lim ? s[x][e] : -__builtin_inff();
       raise(s);
-      u32x4 p[BN / 16];
-      weights(s, p);
-      if (s_bad[kt & 1] != kt + 1) {
+      const bool bad = s_bad[kt & 1] == kt + 1;
 #pragma unroll
-        for (int x = 0; x < BN / 16; x++)
+      for (int x = 0; x < KT; x++) {
+        const int key0 = kt * BN + 32 * x;
+        if (key0 >= n_wave) break;
+        u32x4 p[2];
+        weights(s[x], p);
+        if (!bad) {
 #pragma unroll
-          for (int d = 0; d < DV; d++) acc[d] = mma32<DT>(v_frag(kt, d, x), p[x], acc[d]);
-      } else {
+          for (int y = 0; y < 2; y++)
+#pragma unroll
+            for (int d = 0; d < DV; d++) acc[d] = mma32<DT>(v_frag(kt, d, 2 * x + y), p[y], acc[d]);
+          continue;
+        }
         // key by key, each added only where it is visible
-        for (int j = 0; j < BN; j++) {
-          const int sj = j >> 4, jj = j & 15;
+        for (int j = 0; j < 32; j++) {
+          const int jj = j & 15;
           // the key's place in the operands: half of the wave and element
           const int gj = (jj >> 2) & 1, ej = (jj & 3) + 4 * (jj >> 3);
-          const bool mine = g == gj;
-          u32x4 pj = {0, 0, 0, 0};
-#pragma unroll
-          for (int x = 0; x < BN / 16; x++)
-            if (x == sj) pj = p[x];
           u32x4 keep;
 #pragma unroll
           for (int w = 0; w < 4; w++)
-            keep[w] = (mine && ej >> 1 == w) ? (ej & 1 ? 0xFFFF0000u : 0xFFFFu) : 0u;
-          pj = pj & keep;
+            keep[w] = (g == gj && ej >> 1 == w) ? (ej & 1 ? 0xFFFF0000u : 0xFFFFu) : 0u;
+          const u32x4 pj = (j < 16 ? p[0] : p[1]) & keep;
           const bool vis = key0 + j < lim;
 #pragma unroll
           for (int d = 0; d < DV; d++) {
             f32x16 one;
 #pragma unroll
             for (int e = 0; e < 16; e++) one[e] = 0.0f;
-            one = mma32<DT>(v_frag(kt, d, sj) & keep, pj, one);
+            one = mma32<DT>(v_frag(kt, d, 2 * x + (j >> 4)) & keep, pj, one);
 #pragma unroll
             for (int e = 0; e < 16; e++) acc[d][e] += vis ? one[e] : 0.0f;
           }
         }
       }
-      if (key0 + BN < n_wave) scores(kt + 1, s);
+#pragma unroll
+      for (int x = 0; x < KT; x++)
+        if ((kt + 1) * BN + 32 * x < n_wave) s[x] = scores(kt + 1, x);
     }
-    if (kt + 2 < ntiles) store_k(kt + 2);
     if (kt + 1 < ntiles) store_v(kt + 1);
     __syncthreads();
   }
