@@ -21,12 +21,6 @@
 #include "matrix.h"
 
 #pragma clang fp contract(off)
-#ifndef COLL_PROMPT_OCC
-#define COLL_PROMPT_OCC (NW == 8 ? 2 : 1)
-#endif
-#ifndef COLL_PROMPT_WIDE
-#define COLL_PROMPT_WIDE 1
-#endif
 
 namespace coll {
 namespace {
@@ -57,47 +51,87 @@ __device__ __forceinline__ int32_t span(int64_t a, int64_t b, int64_t n) {
   return (a < 0 || b <= a || b > n) ? 0 : (int32_t)(b - a);
 }
 
-// The sequence that holds query tile `tile` of rank r: every wave scans the
-// sequences' tile counts, 64 at a time.
+// Largest of the lanes' values (below 2^12), a bit at a time.
+__device__ __forceinline__ uint32_t wave_max(uint32_t x) {
+  uint64_t in = ~0ull;
+  uint32_t top = 0;
+#pragma unroll
+  for (int b = 11; b >= 0; b--) {
+    const uint64_t has = __ballot((x >> b) & 1) & in;
+    if (has) {
+      in = has;
+      top |= 1u << b;
+    }
+  }
+  return top;
+}
+
+// The sequence that holds tile slot `slot` of rank r, scanned by every wave, 64
+// sequences at a time.  Causal tiles get longer towards a sequence's end, and
+// the last workgroups to start should be short: up to 64 sequences of up to 64
+// tiles are taken level by level, every sequence's 64th tile first (packed
+// prompts of 1 to 2048 tokens: 148 -> 137 us); others from the last tile down.
 template <int BQ>
-__device__ __forceinline__ TileAt find_tile(const PromptArgs &A, int r, uint32_t tile) {
+__device__ __forceinline__ TileAt find_tile(const PromptArgs &A, int r, uint32_t slot) {
   const int32_t *qs = reinterpret_cast<const int32_t *>(A.q_starts.p[r]);
   const int32_t *ks = reinterpret_cast<const int32_t *>(A.k_starts.p[r]);
   const int32_t *dg = reinterpret_cast<const int32_t *>(A.diag.p[r]);
   const int lane = threadIdx.x & 63;
+  const uint32_t tile = A.tiles - 1 - slot;
   TileAt t{};
   uint32_t before = 0;
   for (int base = 0; base < A.nseq; base += 64) {
     const int b = base + lane;
-    int64_t a0 = 0;
-    int32_t nq = 0;
+    int32_t a0 = 0, a1 = 0, c0 = 0, c1 = 0, d = 0;
     if (b < A.nseq) {
       a0 = qs[b];
-      nq = span(a0, qs[b + 1], A.q_rows);
+      a1 = qs[b + 1];
+      c0 = ks[b];
+      c1 = ks[b + 1];
+      if (dg) d = dg[b];
     }
+    const int32_t nq = span(a0, a1, A.q_rows);
     const uint32_t mine = ((uint32_t)nq + BQ - 1) / BQ;
-    uint32_t upto = mine;
+    int l = -1;
+    uint32_t index = 0;
+    const uint32_t most = A.nseq <= 64 && !__ballot(mine > 64) ? wave_max(mine) : 0;
+    if (most > 0) {
+      uint32_t rest = slot;
+      for (int level = (int)most - 1; level >= 0; level--) {
+        uint64_t in = __ballot(mine > (uint32_t)level);
+        const uint32_t n = (uint32_t)__popcll(in);
+        if (rest < n) {
+          for (; rest > 0; rest--) in &= in - 1;
+          l = __builtin_ctzll(in);
+          index = (uint32_t)level;
+          break;
+        }
+        rest -= n;
+      }
+    } else {
+      uint32_t upto = mine;
 #pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-      const uint32_t x = __shfl_up(upto, d, 64);
-      if (lane >= d) upto += x;
+      for (int x = 1; x < 64; x <<= 1) {
+        const uint32_t y = __shfl_up(upto, x, 64);
+        if (lane >= x) upto += y;
+      }
+      const uint64_t hit = __ballot(before + upto > tile);
+      if (hit) {
+        l = __builtin_ctzll(hit);
+        index = tile - before - (uint32_t)__builtin_amdgcn_readlane((int)(upto - mine), l);
+      }
+      before += (uint32_t)__builtin_amdgcn_readlane((int)upto, 63);
     }
-    const uint64_t hit = __ballot(before + upto > tile);
-    if (hit) {
-      const int l = __builtin_ctzll(hit);
-      const int bb = base + l;
+    if (l >= 0) {
       t.any = true;
-      t.first = (int32_t)((tile - before -
-                           (uint32_t)__builtin_amdgcn_readlane((int)(upto - mine), l)) * BQ);
+      t.first = (int32_t)(index * BQ);
       t.nq = __builtin_amdgcn_readlane(nq, l);
-      t.q0 = __builtin_amdgcn_readfirstlane(qs[bb]);
-      t.k0 = __builtin_amdgcn_readfirstlane(ks[bb]);
-      const int64_t k1 = __builtin_amdgcn_readfirstlane(ks[bb + 1]);
-      t.nk = span(t.k0, k1, A.k_rows);
-      t.diag = dg ? __builtin_amdgcn_readfirstlane(dg[bb]) : t.nk - t.nq;
+      t.q0 = __builtin_amdgcn_readlane(a0, l);
+      t.k0 = __builtin_amdgcn_readlane(c0, l);
+      t.nk = span(t.k0, __builtin_amdgcn_readlane(c1, l), A.k_rows);
+      t.diag = dg ? __builtin_amdgcn_readlane(d, l) : t.nk - t.nq;
       return t;
     }
-    before += (uint32_t)__builtin_amdgcn_readlane((int)upto, 63);
   }
   return t;
 }
@@ -115,7 +149,7 @@ struct Tiles {
 };
 
 template <int DT, int D, int BN, int NW>
-__global__ __launch_bounds__(NW * 64, COLL_PROMPT_OCC) void prompt_tiles(PromptArgs A) {
+__global__ __launch_bounds__(NW * 64, D <= 128 ? 2 : 1) void prompt_tiles(PromptArgs A) {
   constexpr int BQ = NW * 32, CH = D / 8, NT = NW * 64;
   constexpr int NCH = (BN * CH + NT - 1) / NT;        // chunks a thread stages of K and of V
   constexpr bool kWhole = BN * CH % NT == 0;
@@ -132,7 +166,7 @@ __global__ __launch_bounds__(NW * 64, COLL_PROMPT_OCC) void prompt_tiles(PromptA
   if (H % 8 == 0) h = (h & 7) * (H / 8) + (h >> 3);
   const int r = (int)fdiv(th, A.by_tiles);
   const uint32_t tile = A.tiles - 1 - (th - (uint32_t)r * A.tiles);
-  const TileAt t = find_tile<BQ>(A, r, tile);
+  const TileAt t = find_tile<BQ>(A, r, A.tiles - 1 - tile);
   if (!t.any) return;
   const int kvh = (int)fdiv(h, A.by_group);
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -155,15 +189,12 @@ __global__ __launch_bounds__(NW * 64, COLL_PROMPT_OCC) void prompt_tiles(PromptA
   // Q as the B operand: column = query, 8 consecutive elements per lane
   u32x4 q[DK];
   {
+    // (a column past the last row repeats that row and is not stored)
     const char *qp = reinterpret_cast<const char *>(A.q.p[r]) +
-                     ((t.q0 + row) * A.q_stride + (int64_t)h * D) * 2;
+                     ((t.q0 + (row < last_row ? row : last_row)) * A.q_stride + (int64_t)h * D) * 2;
+    const uint32_t sign = A.negate ? 0x80008000u : 0u;
 #pragma unroll
-    for (int s = 0; s < DK; s++) {
-      u32x4 x = {0, 0, 0, 0};
-      if (row <= last_row) x = ld<u32x4>(qp, 2 * s + g);
-      if (A.negate) x = x ^ 0x80008000u;
-      q[s] = x;
-    }
+    for (int s = 0; s < DK; s++) q[s] = ld<u32x4>(qp, 2 * s + g) ^ sign;
   }
 
   // a thread's chunks of a tile: key kr0[i] of the tile, 16 bytes at chunk c
@@ -271,16 +302,28 @@ __global__ __launch_bounds__(NW * 64, COLL_PROMPT_OCC) void prompt_tiles(PromptA
   const int ntiles = (n_block + BN - 1) / BN;
   const int nfull = see_all / BN < ntiles ? see_all / BN : ntiles;   // tiles that need no mask
   if (tid < 2) s_bad[tid] = 0;
-  __syncthreads();
-  if (ntiles > 0) {
-    load(kp, A.k_stride, 0);
-    store_k(0);
-    load(vp, A.v_stride, 0);
-    store_v(0);
-  }
-  if (ntiles > 1) {
-    load(kp, A.k_stride, 1);
-    store_k(1);
+  {
+    // the first tiles of K and V and the second of K, all in flight together
+    u32x4 first[3][NCH];
+#pragma unroll
+    for (int w = 0; w < 3; w++)
+#pragma unroll
+      for (int i = 0; i < NCH; i++) {
+        const int x = tid + i * NT, kr = x / CH, c = x - kr * CH;
+        const int key = (w == 2 ? BN : 0) + kr;
+        u32x4 a = {0, 0, 0, 0};
+        if ((kWhole || x < BN * CH) && key < t.nk && ntiles > 0)
+          a = w == 1 ? ld<u32x4>(vp + key * A.v_stride * 2, c) : ld<u32x4>(kp + key * A.k_stride * 2, c);
+        first[w][i] = a;
+      }
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < 3; w++) {
+#pragma unroll
+      for (int i = 0; i < NCH; i++) held[i] = first[w][i];
+      if (w == 1) store_v(0);
+      else store_k(w >> 1);
+    }
   }
   __syncthreads();
 
@@ -407,19 +450,24 @@ __global__ __launch_bounds__(NW * 64, COLL_PROMPT_OCC) void prompt_tiles(PromptA
 
 template <int DT, int D, int BN>
 int go(const Launch &L, int R, PromptArgs &A, int64_t q_rows) {
-  // 8 waves share a staged tile among 256 rows; 4 (128 rows) when that would
-  // leave compute units without a workgroup
+  // 8 waves share a staged tile among 256 rows when that gives every compute
+  // unit two workgroups' work; otherwise 4 waves and 128 rows, two workgroups
+  // at a time on a compute unit (7476 packed tokens x 32 heads: 136 against
+  // 141 us; 4 x 512 tokens: 38 against 28).  Heads beyond 128 elements leave
+  // registers for 4 waves only.
   const uint64_t tiles8 = (uint64_t)(q_rows + 255) / 256 + A.nseq;
-  const bool wide = COLL_PROMPT_WIDE && tiles8 * A.heads * R >= 2ull * L.num_cus;
+  const bool wide = D <= 128 && tiles8 * A.heads * R >= 2ull * L.num_cus;
   const uint64_t tiles = wide ? tiles8 : (uint64_t)(q_rows + 127) / 128 + A.nseq;
   const uint64_t groups = tiles * A.heads * R;
   if (groups > 0x7FFFFFFFull) return COLL_ERR_UNSUPPORTED;
   A.tiles = (uint32_t)tiles;
   A.by_tiles = make_fastdiv(A.tiles);
-  if (wide)
-    hipLaunchKernelGGL((prompt_tiles<DT, D, BN, 8>), dim3((unsigned)groups), dim3(512), 0, L.stream, A);
-  else
-    hipLaunchKernelGGL((prompt_tiles<DT, D, BN, 4>), dim3((unsigned)groups), dim3(256), 0, L.stream, A);
+  if constexpr (D <= 128)
+    if (wide) {
+      hipLaunchKernelGGL((prompt_tiles<DT, D, BN, 8>), dim3((unsigned)groups), dim3(512), 0, L.stream, A);
+      return hip_status();
+    }
+  hipLaunchKernelGGL((prompt_tiles<DT, D, BN, 4>), dim3((unsigned)groups), dim3(256), 0, L.stream, A);
   return hip_status();
 }
 
