@@ -149,7 +149,7 @@ struct Tiles {
 };
 
 template <int DT, int D, int BN, int NW>
-__global__ __launch_bounds__(NW * 64, D <= 128 ? 2 : 1) void prompt_tiles(PromptArgs A) {
+__global__ __launch_bounds__(NW * 64, D == 64 ? 3 : (D <= 128 ? 2 : 1)) void prompt_tiles(PromptArgs A) {
   constexpr int BQ = NW * 32, CH = D / 8, NT = NW * 64;
   constexpr int NCH = (BN * CH + NT - 1) / NT;        // chunks a thread stages of K and of V
   constexpr bool kWhole = BN * CH % NT == 0;
@@ -337,6 +337,9 @@ __global__ __launch_bounds__(NW * 64, D <= 128 ? 2 : 1) void prompt_tiles(Prompt
 #pragma unroll
     for (int x = 0; x < KT; x++) s[x] = scores(0, x);
   __syncthreads();
+  // the second four waves go first, so that the two of a SIMD do not compute
+  // exponentials at the same time (8192 x 32 heads x 128: 574 -> 567 us)
+  if (wave & 4) __builtin_amdgcn_s_setprio(1);
   int kt = 0;
   for (; kt < nfull; kt++) {
     // K's tile passes through the staging registers in the first half, V's in
@@ -448,21 +451,25 @@ __global__ __launch_bounds__(NW * 64, D <= 128 ? 2 : 1) void prompt_tiles(Prompt
         none ? -__builtin_inff() : (m * A.c + log2_f(l)) * kLn2;
 }
 
+template <int D>
+constexpr bool kWide = D == 96 || D == 128;
+
 template <int DT, int D, int BN>
 int go(const Launch &L, int R, PromptArgs &A, int64_t q_rows) {
   // 8 waves share a staged tile among 256 rows when that gives every compute
   // unit two workgroups' work; otherwise 4 waves and 128 rows, two workgroups
-  // at a time on a compute unit (7476 packed tokens x 32 heads: 136 against
-  // 141 us; 4 x 512 tokens: 38 against 28).  Heads beyond 128 elements leave
-  // registers for 4 waves only.
+  // at a time on a compute unit (7476 packed tokens x 32 heads x 128: 136
+  // against 141 us; 4 x 512 tokens: 38 against 28).  Heads of 64 leave room for
+  // three workgroups of 4 waves (8192 x 32 heads x 64: 337 against 346 us), heads
+  // beyond 128 for one.
   const uint64_t tiles8 = (uint64_t)(q_rows + 255) / 256 + A.nseq;
-  const bool wide = D <= 128 && tiles8 * A.heads * R >= 2ull * L.num_cus;
+  const bool wide = kWide<D> && tiles8 * A.heads * R >= 2ull * L.num_cus;
   const uint64_t tiles = wide ? tiles8 : (uint64_t)(q_rows + 127) / 128 + A.nseq;
   const uint64_t groups = tiles * A.heads * R;
   if (groups > 0x7FFFFFFFull) return COLL_ERR_UNSUPPORTED;
   A.tiles = (uint32_t)tiles;
   A.by_tiles = make_fastdiv(A.tiles);
-  if constexpr (D <= 128)
+  if constexpr (kWide<D>)
     if (wide) {
       hipLaunchKernelGGL((prompt_tiles<DT, D, BN, 8>), dim3((unsigned)groups), dim3(512), 0, L.stream, A);
       return hip_status();

@@ -94,7 +94,8 @@ def fam_prompt():
     prompt_case("zero lengths", 1, 2, 2, 64, [5, 0, 33, 0], [5, 0, 33, 0], tail=3)
     for D, dtype in ((64, "fp16"), (96, "bf16"), (128, "bf16"), (128, "fp16"), (192, "fp16"), (256, "bf16")):
         prompt_case("tiles", 1, 2, 1, D, [130], [130], dtype=dtype, seed=D)
-    prompt_case("eight waves", 1, 8, 4, 64, [300], [300], seed=3)
+    prompt_case("eight waves", 1, 8, 4, 128, [300], [300], seed=3)
+    prompt_case("eight waves, two ranks", 2, 8, 2, 96, [258, 3], [258, 70], seed=4)
     prompt_case("more keys than queries", 1, 2, 1, 128, [70, 3], [200, 65])
     prompt_case("more queries than keys", 1, 2, 1, 64, [70, 9], [20, 0])
     prompt_case("all keys", 1, 3, 3, 96, [40, 65], [129, 7], causal=False)
@@ -113,7 +114,7 @@ def fam_prompt():
     def bad_v(q, k, v):
         v[9], v[70], v[99, :5], k[55] = 0x7F80, 0x7FC1, 0xFF80, 0x7FC1
     prompt_case("infinities and NaN behind the diagonal", 1, 2, 1, 64, [100], [100], plant=bad_v)
-    prompt_case("... and 8 waves", 1, 8, 1, 64, [260], [260], plant=bad_v)
+    prompt_case("... and 8 waves", 1, 8, 1, 128, [260], [260], plant=bad_v)
 
     def bad_tail(q, k, v):
         v[-3:], k[-3:] = 0x7FC1, 0x7F80

@@ -151,6 +151,7 @@ static inline int emu_readlane_at(int v, int lane, const char *f, int l) {
 // The library's matrix.h leaves these to the including environment when
 // COLL_HAVE_MATRIX is defined; layouts as documented there.
 #define COLL_HAVE_MATRIX 1
+#define __builtin_amdgcn_s_setprio(x) ((void)0)
 typedef uint32_t emu_u32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t emu_u32x2 __attribute__((ext_vector_type(2)));
 typedef float emu_f32x4 __attribute__((ext_vector_type(4)));
