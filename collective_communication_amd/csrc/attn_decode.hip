@@ -45,7 +45,7 @@ struct DecodeArgs {
   int64_t num_pages;
   int batch, rows, max_pages, page_size;
   int heads, kv_heads, group, head_tiles;           // head_tiles per kv head
-  int entries;                                      // ranks * batch
+  int ranks, entries;                               // entries: ranks * batch
   FastDiv by_batch, by_page, by_head_tiles, by_wide;
   float c;                                          // |scale| * log2 e
   int negate;
@@ -60,21 +60,46 @@ constexpr int slot_floats() {
   return kHeadTile * D + 2 * kHeadTile;
 }
 
+// p[r] for a lane-dependent r: a select chain over the table in scalar
+// registers.  Indexed, the by-value table becomes a vector load from the
+// argument segment, a round trip to memory before the loads that need it.
+__device__ __forceinline__ const int32_t *pick(const PtrTable &t, int r, int ranks) {
+  uint64_t v = (uint64_t)t.p[0];
+  if (ranks > 1) {
+#pragma unroll
+    for (int q = 1; q < COLL_MAX_RANKS; q++) {
+      uint64_t x = (uint64_t)t.p[q];
+      COLL_SCALAR(x);
+      v = r == q ? x : v;
+    }
+  }
+  return reinterpret_cast<const int32_t *>(v);
+}
+
 // Length of entry e's cache, clipped to what its table row can hold.
 __device__ __forceinline__ int entry_len(const DecodeArgs &A, int e, int *row) {
   const int r = (int)fdiv((uint32_t)e, A.by_batch), b = e - r * A.batch;
-  const int32_t *sq = reinterpret_cast<const int32_t *>(A.seqs.p[r]);
+  const int32_t *sq = pick(A.seqs, r, A.ranks);
   const int x = sq ? sq[b] : b;
   *row = x;
   if (x < 0 || x >= A.rows) return 0;
-  const int64_t n = reinterpret_cast<const int32_t *>(A.lens.p[r])[x];
+  const int64_t n = pick(A.lens, r, A.ranks)[x];
   const int64_t most = (int64_t)A.max_pages * A.page_size;
   return n < 0 ? 0 : (int)(n < most ? n : most);
 }
 __device__ __forceinline__ int units_of(int len) { return len > 0 ? (len + kUnit - 1) / kUnit : 1; }
 
-// First unit of share w of n units in `of` shares.
-__device__ __forceinline__ int share(int64_t n, int w, int of) { return (int)(n * w / of); }
+// n units in `of` shares: the first `odd` of them have each + 1, the others each.
+struct Shares {
+  int each, odd;
+  __device__ Shares(int n, int of) : each((int)((uint32_t)n / (uint32_t)of)), odd(n - each * of) {}
+  __device__ int first(int w) const { return w * each + (w < odd ? w : odd); }
+  __device__ int of(int u) const {                    // the share that holds unit u
+    const uint32_t longer = (uint32_t)odd * (uint32_t)(each + 1);
+    return (uint32_t)u < longer ? (int)((uint32_t)u / (uint32_t)(each + 1))
+                                : odd + (int)(((uint32_t)u - longer) / (uint32_t)each);
+  }
+};
 
 // ND consecutive dwords, non-temporal: the cache is read once (64 ragged caches
 // of 583 MB: 106 us against 120 with plain loads; 128 MB: 34 against 38).
@@ -113,6 +138,10 @@ __global__ __launch_bounds__(256, 2) void decode_split(DecodeArgs A) {
   __shared__ __align__(16) Own s_own[4];
   constexpr bool kQueryLds = ND > 6;
   __shared__ __align__(16) u32x4 s_q[kQueryLds ? ND : 1][64];
+  // (one short cache: 8.3 -> 7.2 us)
+  COLL_FETCH(A.q.p[0], A.k.p[0], A.v.p[0], A.table.p[0], A.lens.p[0], A.seqs.p[0], A.o.p[0],
+             A.lse.p[0]);
+  COLL_FETCH(A.q_stride, A.page_stride, A.num_pages, A.batch, A.heads, A.by_page.m, A.c, A.joins);
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int i16 = lane & 15, g = lane >> 4;
   const int w0 = (int)fdiv(blockIdx.x, A.by_wide), ht = (int)blockIdx.x - w0 * A.heads_wide;
@@ -149,246 +178,253 @@ __global__ __launch_bounds__(256, 2) void decode_split(DecodeArgs A) {
     if (tid == 0) s_pre[0] = carry;
     __syncthreads();
   };
-  scan(0);
-  int total = s_pre[256];
-  if (A.entries > 256) {
-    for (base = 256; base < A.entries; base += 256) {
-      const int carry = s_pre[256];
-      scan(carry);
-    }
-    total = s_pre[256];
-    base = 0;
-    scan(0);
-  }
-  // at most as many shares as there are units, so that each has one and the
-  // joined partials are those of consecutive shares
-  const int W = shares < total ? shares : total;
-  int u = w0 < W ? share(total, w0, W) : 0;
-  const int u1 = w0 < W ? share(total, w0 + 1, W) : 0, begin = u;
+  // The first round over the entries finds the total, and with it this
+  // workgroup's share: at most as many shares as there are units, so that each
+  // has one and the joined partials are those of consecutive shares.
+  bool counting = true;
+  int carry = 0, u = 0, u1 = 0, begin = 0;
+  Shares S(0, 1);
   int4 join = {0, 0, 0, 0};
-
-  while (u < u1) {
-    while (u >= s_pre[256]) {
-      const int carry = s_pre[256];
-      base += 256;
-      scan(carry);
+  for (;;) {
+    scan(carry);
+    const int end = __builtin_amdgcn_readfirstlane(s_pre[256]);
+    if (counting) {
+      if (base + 256 < A.entries) {
+        carry = end;
+        base += 256;
+        continue;
+      }
+      const int W = shares < end ? shares : end;
+      S = Shares(end, W);
+      if (w0 < W) {
+        begin = u = S.first(w0);
+        u1 = S.first(w0 + 1);
+      }
+      counting = false;
+      if (A.entries > 256) {
+        carry = base = 0;
+        continue;
+      }
     }
-    // the entry that holds unit u: the last i with s_pre[i] <= u
-    int lo = 0, hi = 256;
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (s_pre[mid] <= u) lo = mid;
-      else hi = mid;
-    }
-    lo = __builtin_amdgcn_readfirstlane(lo);
-    const int e = base + lo;
-    const int len = __builtin_amdgcn_readfirstlane(s_len[lo]);
-    const int trow = __builtin_amdgcn_readfirstlane(s_row[lo]);
-    const int nu = units_of(len);
-    const int t0 = u - __builtin_amdgcn_readfirstlane(s_pre[lo]);
-    const int t1 = nu < t0 + (u1 - u) ? nu : t0 + (u1 - u);
-    const int r = (int)fdiv((uint32_t)e, A.by_batch), b = e - r * A.batch;
+    while (u < u1 && u < end) {
+      // the entry that holds unit u: as many end at or before it
+      int lo = 0;
+#pragma unroll
+      for (int x = 0; x < 4; x++) lo += __popcll(__ballot(s_pre[64 * x + lane + 1] <= u));
+      lo = __builtin_amdgcn_readfirstlane(lo);
+      const int e = base + lo;
+      const int len = __builtin_amdgcn_readfirstlane(s_len[lo]);
+      const int trow = __builtin_amdgcn_readfirstlane(s_row[lo]);
+      const int nu = units_of(len);
+      const int t0 = u - __builtin_amdgcn_readfirstlane(s_pre[lo]);
+      const int t1 = nu < t0 + (u1 - u) ? nu : t0 + (u1 - u);
+      const int r = (int)fdiv((uint32_t)e, A.by_batch), b = e - r * A.batch;
 
-    // Q as the B operand: column = head, 8 consecutive elements per lane; kept
-    // in LDS where the registers would not hold it too
-    u32x4 q[kQueryLds ? 1 : ND];
+      // Q as the B operand: column = head, 8 consecutive elements per lane; kept
+      // in LDS where the registers would not hold it too
+      u32x4 q[kQueryLds ? 1 : ND];
 #pragma unroll
-    for (int s = 0; s < ND; s++) {
-      u32x4 x = {0, 0, 0, 0};
-      if (i16 < nh)
-        x = ld<u32x4>(reinterpret_cast<const char *>(A.q.p[r]) +
-                          (b * A.q_stride + (int64_t)(h0 + i16) * D) * 2, 4 * s + g);
-      if (A.negate) x = x ^ 0x80008000u;
-      if constexpr (!kQueryLds) q[s] = x;
-      else if (wave == 0) s_q[s][lane] = x;
-    }
-    if constexpr (kQueryLds) __syncthreads();
-    const char *kp = reinterpret_cast<const char *>(A.k.p[r]) + (int64_t)kvh * A.head_stride * 2;
-    const char *vp = reinterpret_cast<const char *>(A.v.p[r]) + (int64_t)kvh * A.head_stride * 2;
-    const int32_t *pages = reinterpret_cast<const int32_t *>(A.table.p[r]) +
-                           (len > 0 ? (int64_t)trow * A.max_pages : 0);
+      for (int s = 0; s < ND; s++) {
+        u32x4 x = {0, 0, 0, 0};
+        if (i16 < nh)
+          x = ld<u32x4>(reinterpret_cast<const char *>(A.q.p[r]) +
+                            (b * A.q_stride + (int64_t)(h0 + i16) * D) * 2, 4 * s + g);
+        if (A.negate) x = x ^ 0x80008000u;
+        if constexpr (!kQueryLds) q[s] = x;
+        else if (wave == 0) s_q[s][lane] = x;
+      }
+      if constexpr (kQueryLds) __syncthreads();
+      const char *kp = reinterpret_cast<const char *>(A.k.p[r]) + (int64_t)kvh * A.head_stride * 2;
+      const char *vp = reinterpret_cast<const char *>(A.v.p[r]) + (int64_t)kvh * A.head_stride * 2;
+      const int32_t *pages = reinterpret_cast<const int32_t *>(A.table.p[r]) +
+                             (len > 0 ? (int64_t)trow * A.max_pages : 0);
 
-    // Pages of the lane's tokens 8 g + j of the chunk at `at`: one look-up where
-    // pages are a multiple of 8 tokens.
-    struct Look {
-      int32_t page[NV];
-    };
-    auto look = [&](int at) -> Look {
-      Look x;
+      // Pages of the lane's tokens 8 g + j of the chunk at `at`: one look-up where
+      // pages are a multiple of 8 tokens.
+      struct Look {
+        int32_t page[NV];
+      };
+      auto look = [&](int at) -> Look {
+        Look x;
 #pragma unroll
-      for (int j = 0; j < NV; j++) {
-        const int t = at + 8 * g + j;
-        x.page[j] = t < len ? pages[fdiv((uint32_t)t, A.by_page)] : -1;
-      }
-      return x;
-    };
-    auto slot_of = [&](int t) -> int { return t - (int)fdiv((uint32_t)t, A.by_page) * A.page_size; };
-    // an absent token reads the pool's first row instead (its score is
-    // masked and its value replaced by 0 before use)
-    auto load = [&](int at, const Look &x) -> Chunk<ND> {
-      Chunk<ND> ch;
-      ch.ok = 0;
-#pragma unroll
-      for (int j = 0; j < 8; j++) {
-        const int t = at + 8 * g + j;
-        const int32_t pg = x.page[P8 ? 0 : j];
-        const bool ok = t < len && pg >= 0 && pg < A.num_pages;
-        const int64_t off = (ok ? pg * A.page_stride + slot_of(t) * A.tok_stride : 0) * 2 + i16 * (4 * ND);
-        ch.ok |= ok ? 1u << j : 0u;
-        ld_row<ND>(kp + off, ch.k[j]);
-        ld_row<ND>(vp + off, ch.v[j]);
-      }
-      return ch;
-    };
-
-    f32x4 acc[2 * ND];
-#pragma unroll
-    for (int x = 0; x < 2 * ND; x++) acc[x] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    float m = -__builtin_inff(), l = 0.0f;
-
-    auto compute = [&](Chunk<ND> &ch) {
-      // row i of K's operand x is token 8 (i / 4) + 4 x + i % 4; a wave's LDS
-      // accesses are in order, so its own piece needs no barrier
-#pragma unroll
-      for (int j = 0; j < 8; j++) {
-        uint32_t *row = s_own[wave].k + (16 * (j >> 2) + 4 * g + (j & 3)) * kKeyRow + i16 * ND;
-#pragma unroll
-        for (int x = 0; x < ND; x++) row[x] = ch.k[j][x];
-      }
-      wave_lds_sync();
-      f32x4 s[2];
-#pragma unroll
-      for (int x = 0; x < 2; x++) {
-        s[x] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-        for (int d = 0; d < ND; d++)
-          s[x] = mma16<DT>(*reinterpret_cast<const u32x4 *>(s_own[wave].k + (16 * x + i16) * kKeyRow +
-                                                            16 * d + 4 * g),
-                         kQueryLds ? s_q[d][lane] : q[kQueryLds ? 0 : d], s[x]);
-      }
-      wave_lds_sync();
-      if (__ballot(ch.ok != 0xFFu)) {
+        for (int j = 0; j < NV; j++) {
+          const int t = at + 8 * g + j;
+          x.page[j] = t < len ? pages[fdiv((uint32_t)t, A.by_page)] : -1;
+        }
+        return x;
+      };
+      auto slot_of = [&](int t) -> int { return t - (int)fdiv((uint32_t)t, A.by_page) * A.page_size; };
+      // an absent token reads the pool's first row instead (its score is
+      // masked and its value replaced by 0 before use)
+      auto load = [&](int at, const Look &x) -> Chunk<ND> {
+        Chunk<ND> ch;
+        ch.ok = 0;
 #pragma unroll
         for (int j = 0; j < 8; j++) {
-          const bool ok = (ch.ok >> j) & 1;
-          s[j >> 2][j & 3] = ok ? s[j >> 2][j & 3] : -__builtin_inff();
-#pragma unroll
-          for (int x = 0; x < ND; x++) ch.v[j][x] = ok ? ch.v[j][x] : 0u;
+          const int t = at + 8 * g + j;
+          const int32_t pg = x.page[P8 ? 0 : j];
+          const bool ok = t < len && pg >= 0 && pg < A.num_pages;
+          const int64_t row = ok ? pg * A.page_stride + slot_of(t) * A.tok_stride : 0;
+          const int64_t off = row * 2 + i16 * (4 * ND);
+          ch.ok |= ok ? 1u << j : 0u;
+          ld_row<ND>(kp + off, ch.k[j]);
+          ld_row<ND>(vp + off, ch.v[j]);
         }
-      }
-      float mt = s[0][0];
-#pragma unroll
-      for (int j = 1; j < 8; j++) mt = fmaxf(mt, s[j >> 2][j & 3]);
-      mt = fmaxf(mt, lane_xor(mt, 16));
-      mt = fmaxf(mt, lane_xor(mt, 32));
-      if (__ballot((mt - m) * A.c > 8.0f)) {
-        const float mn = fmaxf(m, mt);
-        const float f = mn == -__builtin_inff() ? 1.0f : exp2_f((m - mn) * A.c);
-        m = mn;
-        l *= f;
-#pragma unroll
-        for (int x = 0; x < 2 * ND; x++)
-#pragma unroll
-          for (int e2 = 0; e2 < 4; e2++) acc[x][e2] *= f;
-      }
-      const float mc = m == -__builtin_inff() ? 0.0f : m * A.c;
-      float p[8];
-#pragma unroll
-      for (int j = 0; j < 8; j++) {
-        p[j] = exp2_f(__builtin_fmaf(s[j >> 2][j & 3], A.c, -mc));
-        l += p[j];
-      }
-      u32x4 pf;
-#pragma unroll
-      for (int j = 0; j < 4; j++) pf[j] = pack2<DT>(p[2 * j], p[2 * j + 1]);
-#pragma unroll
-      for (int x = 0; x < ND; x++) {
-        u32x4 even, odd;
-#pragma unroll
-        for (int j = 0; j < 4; j++) {
-          even[j] = (ch.v[2 * j][x] & 0xFFFFu) | (ch.v[2 * j + 1][x] << 16);
-          odd[j] = (ch.v[2 * j][x] >> 16) | (ch.v[2 * j + 1][x] & 0xFFFF0000u);
-        }
-        acc[2 * x] = mma16<DT>(even, pf, acc[2 * x]);
-        acc[2 * x + 1] = mma16<DT>(odd, pf, acc[2 * x + 1]);
-      }
-    };
+        return ch;
+      };
 
-    // the wave's chunks, 128 tokens apart.  Page look-ups run one ahead; the
-    // loads do not (with two workgroups on a compute unit there are enough in
-    // flight: a second chunk in registers measured 1% slower).
-    const int stop = len < t1 * kUnit ? len : t1 * kUnit;
-    int at = t0 * kUnit + wave * 32;
-    if (at < stop) {
-      Look nxt = look(at);
-      for (; at < stop; at += kUnit) {
-        Chunk<ND> cur = load(at, nxt);
-        nxt = look(at + kUnit);
-        compute(cur);
-      }
-    }
+      f32x4 acc[2 * ND];
+#pragma unroll
+      for (int x = 0; x < 2 * ND; x++) acc[x] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+      float m = -__builtin_inff(), l = 0.0f;
 
-    // join the four waves: weights exp2((m_w - m) c), then one sum per output
-    l += lane_xor(l, 16);
-    l += lane_xor(l, 32);
-    if (g == 0) {
-      s_m[wave][i16] = m;
-      s_l[wave][i16] = l;
-    }
-    __syncthreads();
-    float mm = s_m[0][i16];
+      auto compute = [&](Chunk<ND> &ch) {
+        // row i of K's operand x is token 8 (i / 4) + 4 x + i % 4; a wave's LDS
+        // accesses are in order, so its own piece needs no barrier
 #pragma unroll
-    for (int w = 1; w < 4; w++) mm = fmaxf(mm, s_m[w][i16]);
-    {
-      const float f = m == -__builtin_inff() ? (l != l ? l : 0.0f) : exp2_f((m - mm) * A.c);
+        for (int j = 0; j < 8; j++) {
+          uint32_t *row = s_own[wave].k + (16 * (j >> 2) + 4 * g + (j & 3)) * kKeyRow + i16 * ND;
 #pragma unroll
-      for (int rr = 0; rr < 4; rr++)
+          for (int x = 0; x < ND; x++) row[x] = ch.k[j][x];
+        }
+        wave_lds_sync();
+        f32x4 s[2];
 #pragma unroll
-        for (int x = 0; x < 2 * ND; x++) s_own[wave].o[i16][2 * ND * (4 * g + rr) + x] = acc[x][rr] * f;
-    }
-    __syncthreads();
-    const bool whole = t0 == 0 && t1 == nu;
-    const int slot = 2 * (int)blockIdx.x + (u == begin ? 0 : 1);
-    float *ps = A.part + (int64_t)slot * slot_floats<D>();
-    for (int x = tid; x < nh * (D / 2); x += 256) {
-      const int hh = x / (D / 2), d = 2 * (x - hh * (D / 2));
-      float M = s_m[0][hh];
+        for (int x = 0; x < 2; x++) {
+          s[x] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-      for (int w = 1; w < 4; w++) M = fmaxf(M, s_m[w][hh]);
-      float y0 = 0.0f, y1 = 0.0f, ll = 0.0f;
+          for (int d = 0; d < ND; d++)
+            s[x] = mma16<DT>(*reinterpret_cast<const u32x4 *>(s_own[wave].k + (16 * x + i16) * kKeyRow +
+                                                              16 * d + 4 * g),
+                           kQueryLds ? s_q[d][lane] : q[kQueryLds ? 0 : d], s[x]);
+        }
+        wave_lds_sync();
+        if (__ballot(ch.ok != 0xFFu)) {
 #pragma unroll
-      for (int w = 0; w < 4; w++) {
-        const float mw = s_m[w][hh], lw = s_l[w][hh];
-        ll += mw == -__builtin_inff() ? (lw != lw ? lw : 0.0f) : lw * exp2_f((mw - M) * A.c);
-        y0 += s_own[w].o[hh][d];
-        y1 += s_own[w].o[hh][d + 1];
-      }
-      if (whole) {
-        const bool none = ll == 0.0f;
-        const float inv = none ? 0.0f : 1.0f / ll;
-        char *op = reinterpret_cast<char *>(A.o.p[r]) + (b * A.o_stride + (int64_t)(h0 + hh) * D + d) * 2;
-        *reinterpret_cast<uint32_t *>(op) = none ? 0u : pack2<DT>(y0 * inv, y1 * inv);
-        if (d == 0 && A.lse.p[r])
-          reinterpret_cast<float *>(A.lse.p[r])[(int64_t)b * A.heads + h0 + hh] =
-              none ? -__builtin_inff() : (M * A.c + log2_f(ll)) * kLn2;
-      } else {
-        ps[hh * D + d] = y0;
-        ps[hh * D + d + 1] = y1;
-        if (d == 0) {
-          ps[kHeadTile * D + hh] = M;
-          ps[kHeadTile * D + kHeadTile + hh] = ll;
+          for (int j = 0; j < 8; j++) {
+            const bool ok = (ch.ok >> j) & 1;
+            s[j >> 2][j & 3] = ok ? s[j >> 2][j & 3] : -__builtin_inff();
+#pragma unroll
+            for (int x = 0; x < ND; x++) ch.v[j][x] = ok ? ch.v[j][x] : 0u;
+          }
+        }
+        float mt = s[0][0];
+#pragma unroll
+        for (int j = 1; j < 8; j++) mt = fmaxf(mt, s[j >> 2][j & 3]);
+        mt = fmaxf(mt, lane_xor(mt, 16));
+        mt = fmaxf(mt, lane_xor(mt, 32));
+        if (__ballot((mt - m) * A.c > 8.0f)) {
+          const float mn = fmaxf(m, mt);
+          const float f = mn == -__builtin_inff() ? 1.0f : exp2_f((m - mn) * A.c);
+          m = mn;
+          l *= f;
+#pragma unroll
+          for (int x = 0; x < 2 * ND; x++)
+#pragma unroll
+            for (int e2 = 0; e2 < 4; e2++) acc[x][e2] *= f;
+        }
+        const float mc = m == -__builtin_inff() ? 0.0f : m * A.c;
+        float p[8];
+#pragma unroll
+        for (int j = 0; j < 8; j++) {
+          p[j] = exp2_f(__builtin_fmaf(s[j >> 2][j & 3], A.c, -mc));
+          l += p[j];
+        }
+        u32x4 pf;
+#pragma unroll
+        for (int j = 0; j < 4; j++) pf[j] = pack2<DT>(p[2 * j], p[2 * j + 1]);
+#pragma unroll
+        for (int x = 0; x < ND; x++) {
+          u32x4 even, odd;
+#pragma unroll
+          for (int j = 0; j < 4; j++) {
+            even[j] = (ch.v[2 * j][x] & 0xFFFFu) | (ch.v[2 * j + 1][x] << 16);
+            odd[j] = (ch.v[2 * j][x] >> 16) | (ch.v[2 * j + 1][x] & 0xFFFF0000u);
+          }
+          acc[2 * x] = mma16<DT>(even, pf, acc[2 * x]);
+          acc[2 * x + 1] = mma16<DT>(odd, pf, acc[2 * x + 1]);
+        }
+      };
+
+      // the wave's chunks, 128 tokens apart.  Page look-ups run one ahead; the
+      // loads do not (with two workgroups on a compute unit there are enough in
+      // flight: a second chunk in registers measured 1% slower).
+      const int stop = len < t1 * kUnit ? len : t1 * kUnit;
+      int at = t0 * kUnit + wave * 32;
+      if (at < stop) {
+        Look nxt = look(at);
+        for (; at < stop; at += kUnit) {
+          Chunk<ND> cur = load(at, nxt);
+          nxt = look(at + kUnit);
+          compute(cur);
         }
       }
+
+      // join the four waves: weights exp2((m_w - m) c), then one sum per output
+      l += lane_xor(l, 16);
+      l += lane_xor(l, 32);
+      if (g == 0) {
+        s_m[wave][i16] = m;
+        s_l[wave][i16] = l;
+      }
+      __syncthreads();
+      float mm = s_m[0][i16];
+#pragma unroll
+      for (int w = 1; w < 4; w++) mm = fmaxf(mm, s_m[w][i16]);
+      {
+        const float f = m == -__builtin_inff() ? (l != l ? l : 0.0f) : exp2_f((m - mm) * A.c);
+#pragma unroll
+        for (int rr = 0; rr < 4; rr++)
+#pragma unroll
+          for (int x = 0; x < 2 * ND; x++)
+            s_own[wave].o[i16][2 * ND * (4 * g + rr) + x] = acc[x][rr] * f;
+      }
+      __syncthreads();
+      const bool whole = t0 == 0 && t1 == nu;
+      const int slot = 2 * (int)blockIdx.x + (u == begin ? 0 : 1);
+      float *ps = A.part + (int64_t)slot * slot_floats<D>();
+      for (int x = tid; x < nh * (D / 2); x += 256) {
+        const int hh = x / (D / 2), d = 2 * (x - hh * (D / 2));
+        float M = s_m[0][hh];
+#pragma unroll
+        for (int w = 1; w < 4; w++) M = fmaxf(M, s_m[w][hh]);
+        float y0 = 0.0f, y1 = 0.0f, ll = 0.0f;
+#pragma unroll
+        for (int w = 0; w < 4; w++) {
+          const float mw = s_m[w][hh], lw = s_l[w][hh];
+          ll += mw == -__builtin_inff() ? (lw != lw ? lw : 0.0f) : lw * exp2_f((mw - M) * A.c);
+          y0 += s_own[w].o[hh][d];
+          y1 += s_own[w].o[hh][d + 1];
+        }
+        if (whole) {
+          const bool none = ll == 0.0f;
+          const float inv = none ? 0.0f : 1.0f / ll;
+          char *op = reinterpret_cast<char *>(A.o.p[r]) +
+                     (b * A.o_stride + (int64_t)(h0 + hh) * D + d) * 2;
+          *reinterpret_cast<uint32_t *>(op) = none ? 0u : pack2<DT>(y0 * inv, y1 * inv);
+          if (d == 0 && A.lse.p[r])
+            reinterpret_cast<float *>(A.lse.p[r])[(int64_t)b * A.heads + h0 + hh] =
+                none ? -__builtin_inff() : (M * A.c + log2_f(ll)) * kLn2;
+        } else {
+          ps[hh * D + d] = y0;
+          ps[hh * D + d + 1] = y1;
+          if (d == 0) {
+            ps[kHeadTile * D + hh] = M;
+            ps[kHeadTile * D + kHeadTile + hh] = ll;
+          }
+        }
+      }
+      if (t0 == 0 && !whole) {
+        // the entry's units end in another share: that many partials
+        const int w = S.of(u + nu - 1);
+        join = int4{w - w0 + 1, slot, e, 0};
+      }
+      __syncthreads();
+      u += t1 - t0;
     }
-    if (t0 == 0 && !whole) {
-      // the entry's units end in another share: that many partials
-      int64_t last = (int64_t)u + nu - 1;
-      int w = (int)(last * W / total);
-      while (share(total, w + 1, W) <= last) w++;
-      join = int4{w - w0 + 1, slot, e, 0};
-    }
-    __syncthreads();
-    u += t1 - t0;
+    if (u >= u1) break;
+    carry = end;
+    base += 256;
   }
   if (tid == 0) A.joins[blockIdx.x] = join;
 }
@@ -403,6 +439,7 @@ __global__ __launch_bounds__(kJoinLanes) void decode_join(DecodeArgs A) {
   constexpr int LR = D / 4, RW = kJoinLanes / LR;     // lanes of a row (4 floats each), rows at a time
   __shared__ float s_f[kMaxSplit], s_m[NW], s_l[NW];
   __shared__ __align__(16) f32x4 s_o[RW][LR];
+  COLL_FETCH(A.joins, A.part, A.o.p[0], A.lse.p[0], A.o_stride, A.heads, A.by_wide.m, A.c);
   const int hh = (int)blockIdx.y;
   const int4 join = A.joins[blockIdx.x];
   const int n = __builtin_amdgcn_readfirstlane(join.x);
@@ -414,7 +451,8 @@ __global__ __launch_bounds__(kJoinLanes) void decode_join(DecodeArgs A) {
   if (hh >= nh) return;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   auto slot_at = [&](int i) -> const float * {
-    return A.part + (int64_t)(i == 0 ? join.y : 2 * ((int)blockIdx.x + i * A.heads_wide)) * slot_floats<D>();
+    const int slot = i == 0 ? join.y : 2 * ((int)blockIdx.x + i * A.heads_wide);
+    return A.part + (int64_t)slot * slot_floats<D>();
   };
   const int h = kvh * A.group + part * kHeadTile + hh;
   char *op = reinterpret_cast<char *>(A.o.p[r]) + (b * A.o_stride + (int64_t)h * D) * 2;
@@ -581,10 +619,11 @@ int launch_attn_decode(const Launch &L, int R, const PtrTable &q, const PtrTable
   A.q_stride = q_stride, A.o_stride = o_stride;
   A.page_stride = page_stride, A.tok_stride = tok_stride, A.head_stride = head_stride;
   A.num_pages = num_pages;
-  A.batch = batch, A.rows = num_pages > 0 && max_pages > 0 ? rows : 0, A.max_pages = max_pages, A.page_size = page_size;
+  A.batch = batch, A.rows = num_pages > 0 && max_pages > 0 ? rows : 0;
+  A.max_pages = max_pages, A.page_size = page_size;
   A.heads = heads, A.kv_heads = kv_heads, A.group = heads / kv_heads;
   A.head_tiles = (A.group + kHeadTile - 1) / kHeadTile;
-  A.entries = R * batch;
+  A.ranks = R, A.entries = R * batch;
   A.by_batch = make_fastdiv((uint32_t)batch);
   A.by_page = make_fastdiv((uint32_t)page_size);
   A.by_head_tiles = make_fastdiv((uint32_t)A.head_tiles);
@@ -594,7 +633,8 @@ int launch_attn_decode(const Launch &L, int R, const PtrTable &q, const PtrTable
   A.by_wide = make_fastdiv((uint32_t)wide);
   const size_t W = (size_t)split_of(units, wide);
   A.joins = reinterpret_cast<int4 *>(ws);
-  A.part = reinterpret_cast<float *>(reinterpret_cast<char *>(ws) + (W * sizeof(int4) + 255) / 256 * 256);
+  A.part = reinterpret_cast<float *>(reinterpret_cast<char *>(ws) +
+                                     (W * sizeof(int4) + 255) / 256 * 256);
   const bool splits = max_len > kUnit;
 #define COLL_DECODE(DTV)                                   \
   switch (D) {                                             \

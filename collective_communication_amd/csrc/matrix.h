@@ -68,6 +68,14 @@ __device__ __forceinline__ float max_halves(float x) {
 }
 #endif
 
+// Kernel arguments taken to be needed here, all at once: a struct of tables
+// spans many cache lines, and lines first touched where their values are used
+// cost a trip to memory each, one after the other.  Emits no instruction.
+#ifndef COLL_FETCH
+#define COLL_FETCH(a, b, c, d, e, f, g, h) \
+  asm volatile("" ::"s"(a), "s"(b), "s"(c), "s"(d), "s"(e), "s"(f), "s"(g), "s"(h))
+#endif
+
 // Two fp32 -> a pair of the 16-bit type, round to nearest even.
 template <int DT>
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
