@@ -802,6 +802,13 @@ def _ptrs(ts, what, R):
     return (ctypes.c_void_p * R)(*[t.data_ptr() for t in ts])
 
 
+def _each(ts, what, R):
+    """The first of R tensors (one per rank)."""
+    if len(ts) != R:
+        raise ValueError(f"{what}: {len(ts)} buffers for {R} ranks (one per rank)")
+    return ts[0]
+
+
 def _ints(ts, shape, what, R):
     """R contiguous int32 tensors of one shape."""
     for t in ts:
@@ -877,7 +884,7 @@ def attn_prompt(qs, ks, vs, outs, q_starts, k_starts, lses=None, diags=None, cau
     written."""
     R = _ranks(qs, "attn_prompt")
     dt = _attn_dtype(qs[0], "attn_prompt")
-    if qs[0].dim() != 3 or not ks or ks[0].dim() != 3:
+    if qs[0].dim() != 3 or _each(ks, "k", R).dim() != 3:
         raise ValueError("attn_prompt: q and k are [tokens, heads, head_dim]")
     Tq, H, D = qs[0].shape
     Tk, KV = ks[0].shape[:2]
@@ -887,7 +894,7 @@ def attn_prompt(qs, ks, vs, outs, q_starts, k_starts, lses=None, diags=None, cau
     k, k_stride = _heads_rows(ks, (Tk, KV, D), qs[0].dtype, "k", R)
     v, v_stride = _heads_rows(vs, (Tk, KV, D), qs[0].dtype, "v", R)
     o, o_stride = _heads_rows(outs, (Tq, H, D), qs[0].dtype, "out", R)
-    n = q_starts[0].numel() - 1
+    n = _each(q_starts, "q_starts", R).numel() - 1
     if n < 0:
         raise ValueError("attn_prompt: starts have one entry more than there are sequences")
     qst, kst = _ints(q_starts, (n + 1,), "q_starts", R), _ints(k_starts, (n + 1,), "k_starts", R)
@@ -935,7 +942,7 @@ def attn_decode(qs, k_pools, v_pools, tables, lens, outs, workspace, lses=None, 
 
 
 def _rows_of_cache(tables, lens, seqs, batch, what, R):
-    if tables[0].dim() != 2:
+    if _each(tables, "tables", R).dim() != 2:
         raise ValueError(f"{what}: tables are int32 [rows, max_pages]")
     rows, width = tables[0].shape
     tab, ln = _ints(tables, (rows, width), "tables", R), _ints(lens, (rows,), "lens", R)
@@ -960,7 +967,7 @@ def kv_write(ks, vs, k_pools, v_pools, tables, lens, starts, seqs=None, stream=N
     kp, vp, (N, P, KVp, Dp), strides = _pool_tables(k_pools, v_pools, ks[0].dtype, "kv_write", R)
     if (KVp, Dp) != (KV, D):
         raise ValueError("kv_write: the pools' heads differ from the tokens'")
-    B = starts[0].numel() - 1
+    B = _each(starts, "starts", R).numel() - 1
     if B < 0:
         raise ValueError("kv_write: starts have one entry more than there are sequences")
     st = _ints(starts, (B + 1,), "starts", R)

@@ -177,3 +177,27 @@ def test_binding_refuses_before_it_asks_the_library():
         coll._kv_moves(torch.zeros(1, 2, dtype=torch.int32), st[0], 2, "kv_fork")
     with pytest.raises(ValueError, match="one shape|same shape|pools are"):
         coll.kv_copy_pages([torch.zeros(4, 3), torch.zeros(4, 2)], torch.zeros(1, 2, dtype=torch.int32))
+
+
+def test_binding_wants_one_buffer_per_rank():
+    bf = torch.bfloat16
+    q, k = [torch.zeros(4, 4, 64, dtype=bf)], [torch.zeros(4, 2, 64, dtype=bf)]
+    for call in (lambda: coll.attn_prompt(q, [], k, q, [], []), lambda: coll.attn_prompt([], k, k, q, [], []),
+                 lambda: coll._rows_of_cache([], [], None, 1, "attn_decode", 1),
+                 lambda: coll._ints([], (1,), "lens", 1), lambda: coll._each([], "starts", 1)):
+        with pytest.raises(ValueError, match="rank"):
+            call()
+
+
+def test_a_plan_keeps_the_pointer_tables_it_converted():
+    """The converted arguments hold the tables: their contents survive the lists
+    they came from."""
+    import gc
+    a = (ctypes.c_void_p * 3)(11, 22, 33)
+    kept = coll._as_c(a, ctypes.c_void_p)
+    del a
+    gc.collect()
+    junk = [(ctypes.c_void_p * 3)(7, 7, 7) for _ in range(1000)]
+    assert list((ctypes.c_void_p * 3).from_address(kept.value)) == [11, 22, 33] and junk
+    assert coll._as_c(5, ctypes.c_int).value == 5 and coll._as_c(None, ctypes.c_void_p) is None
+    assert coll._as_c(0x1234, ctypes.c_void_p).value == 0x1234

@@ -148,6 +148,43 @@ def test_prompt_reads_a_fused_projection_and_writes_a_strided_output():
     assert (got[:, H:] == POISON).all()
 
 
+def test_prompt_without_keys():
+    """No key rows at all: every output row is empty."""
+    say("attn_prompt, no keys")
+    q, kv = up(np.zeros((9, 4, 64), np.uint16), "bf16"), torch.empty((0, 2, 64), dtype=torch.bfloat16, device="cuda")
+    out, lse = poisoned((9, 4, 64), "bf16"), torch.zeros((9, 4), device="cuda")
+    coll.attn_prompt([q], [kv], [kv], [out], [i32([0, 4, 9])], [i32([0, 0, 0])], lses=[lse])
+    coll.attn_prompt([q[:0]], [kv], [kv], [out[:0]], [i32([0])], [i32([0])])
+    torch.cuda.synchronize()
+    assert (host(out) == 0).all() and np.isneginf(host(lse)).all()
+
+
+def test_prompt_offsets_past_32_bits():
+    """Rows whose elements lie beyond 2^31 of their buffer, 4.9 GB away."""
+    say("attn_prompt, far rows")
+    T, stride, H, KV, D, n = 61000, 40000, 4, 2, 64, 150
+    buf = torch.empty(T * stride, dtype=torch.bfloat16, device="cuda")
+    rows = buf.view(T, stride)[:, :(2 * H + 2 * KV) * D].view(T, 2 * H + 2 * KV, D)
+    b = ref.normal(np.random.default_rng(5), (n, H + 2 * KV, D), "bf16")
+    rows[T - n:, :H + 2 * KV] = up(b, "bf16")
+    out, lse = rows[:, H + 2 * KV:], torch.empty((T, H), device="cuda")
+    st = i32([T - n, T - 40, T])
+    coll.attn_prompt([rows[:, :H]], [rows[:, H:H + KV]], [rows[:, H + KV:H + 2 * KV]], [out], [st], [st],
+                     lses=[lse])
+    torch.cuda.synchronize()
+    want = ref.prompt(b[:, :H], b[:, H:H + KV], b[:, H + KV:], [0, n - 40, n], [0, n - 40, n], None, True,
+                      D ** -0.5, "bf16")
+    ref.check("far rows", host(out[T - n:]), host(lse[T - n:]), *want[:4], "bf16")
+
+
+def test_prompt_many_heads_and_ranks():
+    run_prompt("16 ranks", 16, 2, 1, 64, [70, 3], [70, 3], seed=21)
+    run_prompt("one kv head each", 1, 100, 100, 64, [33], [33], seed=22)
+    run_prompt("65 sequences, one long", 1, 2, 1, 96, [1000] + [2] * 64, [1000] + [2] * 64, seed=23)
+    run_prompt("64 sequences, tiles of all levels", 1, 8, 8, 128, [i * 11 for i in range(64)],
+               [i * 11 for i in range(64)], seed=24)
+
+
 # --------------------------------------------------------------------- decode
 
 def make_cache(g, R, kv, D, lens, P, dtype, width=None, spare=2):
@@ -218,6 +255,13 @@ def test_decode_ranks_and_batches():
     run_decode("300 entries", 2, 2, 2, 64, [1 + (37 * i) % 400 for i in range(300)], 16, seed=3)
     run_decode("more entries than workgroups", 4, 2, 2, 64, [i % 3 for i in range(260)], 8, seed=4)
     run_decode("nothing at all", 2, 2, 1, 64, [0, 0, 0], 8, seed=5)
+
+
+def test_decode_16_ranks_and_wide_batches():
+    run_decode("16 ranks", 16, 2, 1, 64, [40, 300], 16, seed=31)
+    run_decode("600 heads", 1, 600, 600, 64, [40, 300], 16, seed=32)
+    run_decode("600 heads, split", 1, 600, 600, 64, [400], 16, seed=33, width=200)
+    run_decode("1000 entries", 1, 2, 1, 64, [(13 * i) % 300 for i in range(1000)], 16, "fp16", seed=34)
 
 
 def test_decode_rows_by_name_and_layouts():
