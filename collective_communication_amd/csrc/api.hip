@@ -725,8 +725,8 @@ int coll_attn_prompt(int R, const void *const *q, const void *const *k, const vo
                      int causal, float scale, coll_dtype_t dtype, void *stream) {
   const int st = attn_check(R, heads, kv_heads, head_dim, scale, dtype);
   if (st != COLL_OK) return st;
-  if (nseq < 0 || q_rows < 0 || k_rows < 0 || q_rows >= ((int64_t)1 << 31) ||
-      k_rows >= ((int64_t)1 << 31))
+  const int64_t most = ((int64_t)1 << 31) - 1024;     // room for a tile in 32 bits
+  if (nseq < 0 || q_rows < 0 || k_rows < 0 || q_rows > most || k_rows > most)
     return COLL_ERR_INVALID_ARG;
   if (nseq == 0 || q_rows == 0) return COLL_OK;
   const int64_t qw = (int64_t)heads * head_dim, kw = (int64_t)kv_heads * head_dim;

@@ -136,25 +136,34 @@ __device__ __forceinline__ TileAt find_tile(const PromptArgs &A, int r, uint32_t
   return t;
 }
 
-// BN keys in LDS, two tiles of K and two of V.  The rows are padded so that
+// Waves that share 32 query rows.  Beyond 128 elements the registers of a wave
+// that holds whole rows would leave a SIMD one wave; two waves then compute the
+// same scores and weights, and each half of the output's columns (4096 causal
+// tokens x 16 heads x 256: 251 us against 390, x 192: 189 against 220).
+template <int D>
+constexpr int kSplit = D > 128 ? 2 : 1;
+
+constexpr int BN = 64;                 // keys of a tile
+
+// A tile's keys in LDS, two tiles of K and two of V.  The rows are padded so that
 // neither the row reads of K (8 lanes, 16 bytes of 8 consecutive rows: a
 // stride of 4 mod 32 banks) nor the column reads of V (32 lanes, 64 bytes of
 // 4 consecutive rows: 16 or 48 mod 64 banks) meet bank conflicts; a lane's
 // address is then one base and a constant.
-template <int D, int BN>
+template <int D>
 struct Tiles {
   static constexpr int kRowK = D + 8, kRowV = D % 64 == 0 ? D + 32 : D;   // elements
   uint16_t k[2][BN * kRowK];
   uint16_t v[2][BN * kRowV];
 };
 
-template <int DT, int D, int BN, int NW>
-__global__ __launch_bounds__(NW * 64, D == 64 ? 3 : (D <= 128 ? 2 : 1)) void prompt_tiles(PromptArgs A) {
-  constexpr int BQ = NW * 32, CH = D / 8, NT = NW * 64;
+template <int DT, int D, int NW>
+__global__ __launch_bounds__(NW * 64, D == 64 ? 3 : 2) void prompt_tiles(PromptArgs A) {
+  constexpr int SP = kSplit<D>, BQ = NW / SP * 32, CH = D / 8, NT = NW * 64;
   constexpr int NCH = (BN * CH + NT - 1) / NT;        // chunks a thread stages of K and of V
   constexpr bool kWhole = BN * CH % NT == 0;
-  constexpr int DK = D / 16, DV = D / 32, KT = BN / 32;
-  using TL = Tiles<D, BN>;
+  constexpr int DK = D / 16, DV = D / 32 / SP, KT = BN / 32;
+  using TL = Tiles<D>;
   __shared__ __align__(16) TL s_t;
   __shared__ int s_bad[2];                            // 1 + index of a tile whose V is not finite
   // heads vary fastest, and in steps that keep the heads of one kv head on
@@ -181,7 +190,8 @@ __global__ __launch_bounds__(NW * 64, D == 64 ? 3 : (D <= 128 ? 2 : 1)) void pro
   const int last_row = (t.first + BQ < t.nq ? t.first + BQ : t.nq) - 1;
   const int n_block = limit(last_row);                // keys any row of the tile sees
   const int see_all = limit(t.first);                 // keys every row of the tile sees
-  const int row0 = t.first + wave * 32;               // the wave's rows
+  const int row0 = t.first + wave / SP * 32;          // the wave's rows
+  const int d0 = wave % SP * DV;                      // and its first 32 columns of V
   const int row = row0 + col;
   const int n_wave = row0 <= last_row ? limit(row0 + 31 < last_row ? row0 + 31 : last_row) : 0;
   const int lim = limit(row);
@@ -255,7 +265,7 @@ __global__ __launch_bounds__(NW * 64, D == 64 ? 3 : (D <= 128 ? 2 : 1)) void pro
   };
   // V^T as the A operand of rows 32 d.., keys 16 s ..: two transposing reads,
   // keys 16 s + 4 g + 0..3 and those 8 further on
-  const int vat = (4 * g + ((lane & 15) >> 2)) * TL::kRowV + (lane & 16) + 4 * (lane & 3);
+  const int vat = (4 * g + ((lane & 15) >> 2)) * TL::kRowV + (lane & 16) + 4 * (lane & 3) + 32 * d0;
   auto v_frag = [&](int kt, int d, int s) -> u32x4 {
     const uint16_t *p = s_t.v[kt & 1] + vat + 16 * s * TL::kRowV + 32 * d;
     const u32x2 x = lds_tr16(p), y = lds_tr16(p + 8 * TL::kRowV);
@@ -444,17 +454,14 @@ __global__ __launch_bounds__(NW * 64, D == 64 ? 3 : (D <= 128 ? 2 : 1)) void pro
 #pragma unroll
       for (int w = 0; w < 4; w++) y[w] = none ? 0.0f : acc[d][e + w] * inv;
       u32x2 w2 = {pack2<DT>(y[0], y[1]), pack2<DT>(y[2], y[3])};
-      st<u32x2>(op, (32 * d + 2 * e + 4 * g) / 4, w2);
+      st<u32x2>(op, (32 * (d0 + d) + 2 * e + 4 * g) / 4, w2);
     }
-  if (A.lse.p[r] && g == 0)
+  if (A.lse.p[r] && g == 0 && d0 == 0)
     reinterpret_cast<float *>(A.lse.p[r])[(t.q0 + row) * A.heads + h] =
         none ? -__builtin_inff() : (m * A.c + log2_f(l)) * kLn2;
 }
 
-template <int D>
-constexpr bool kWide = D == 96 || D == 128;
-
-template <int DT, int D, int BN>
+template <int DT, int D>
 int go(const Launch &L, int R, PromptArgs &A, int64_t q_rows) {
   // 8 waves share a staged tile among 256 rows when that gives every compute
   // unit two workgroups' work; otherwise 4 waves and 128 rows, two workgroups
@@ -463,18 +470,21 @@ int go(const Launch &L, int R, PromptArgs &A, int64_t q_rows) {
   // three workgroups of 4 waves (8192 x 32 heads x 64: 337 against 346 us), heads
   // beyond 128 for one.
   const uint64_t tiles8 = (uint64_t)(q_rows + 255) / 256 + A.nseq;
-  const bool wide = kWide<D> && tiles8 * A.heads * R >= 2ull * L.num_cus;
+  const bool wide = (D == 96 || D == 128) && tiles8 * A.heads * R >= 2ull * L.num_cus;
   const uint64_t tiles = wide ? tiles8 : (uint64_t)(q_rows + 127) / 128 + A.nseq;
   const uint64_t groups = tiles * A.heads * R;
   if (groups > 0x7FFFFFFFull) return COLL_ERR_UNSUPPORTED;
   A.tiles = (uint32_t)tiles;
   A.by_tiles = make_fastdiv(A.tiles);
-  if constexpr (kWide<D>)
-    if (wide) {
-      hipLaunchKernelGGL((prompt_tiles<DT, D, BN, 8>), dim3((unsigned)groups), dim3(512), 0, L.stream, A);
+  // D = 96 and 128: both forms; 64: 4 waves; 192 and 256: 8 waves, two to a row
+  if constexpr (D > 64) {
+    if (wide || D > 128) {
+      hipLaunchKernelGGL((prompt_tiles<DT, D, 8>), dim3((unsigned)groups), dim3(512), 0, L.stream, A);
       return hip_status();
     }
-  hipLaunchKernelGGL((prompt_tiles<DT, D, BN, 4>), dim3((unsigned)groups), dim3(256), 0, L.stream, A);
+  }
+  if constexpr (D <= 128)
+    hipLaunchKernelGGL((prompt_tiles<DT, D, 4>), dim3((unsigned)groups), dim3(256), 0, L.stream, A);
   return hip_status();
 }
 
@@ -498,11 +508,11 @@ int launch_attn_prompt(const Launch &L, int R, const PtrTable &q, const PtrTable
   A.c = __builtin_fabsf(scale) * kLog2e;
 #define COLL_PROMPT(DTV)                                              \
   switch (D) {                                                        \
-    case 64: return go<DTV, 64, 64>(L, R, A, q_rows);                 \
-    case 96: return go<DTV, 96, 64>(L, R, A, q_rows);                 \
-    case 128: return go<DTV, 128, 64>(L, R, A, q_rows);               \
-    case 192: return go<DTV, 192, 32>(L, R, A, q_rows);               \
-    case 256: return go<DTV, 256, 32>(L, R, A, q_rows);               \
+    case 64: return go<DTV, 64>(L, R, A, q_rows);                 \
+    case 96: return go<DTV, 96>(L, R, A, q_rows);                 \
+    case 128: return go<DTV, 128>(L, R, A, q_rows);               \
+    case 192: return go<DTV, 192>(L, R, A, q_rows);               \
+    case 256: return go<DTV, 256>(L, R, A, q_rows);               \
     default: return COLL_ERR_UNSUPPORTED;                             \
   }
   if (dt == COLL_BF16) { COLL_PROMPT(COLL_BF16) }

@@ -606,7 +606,7 @@ int coll_moe_combine_recv(int nranks, const void *const *recvbufs, const int32_t
  * query rows do not all lie in [0, q_rows) is not computed; one whose key
  * rows do not all lie in [0, k_rows) has no keys.
  * The launch has a workgroup for each 256 (or 128) query rows and one more per
- * sequence, for each head; q_rows, k_rows < 2^31.
+ * sequence, for each head; q_rows and k_rows are at most 2^31 - 1024.
  */
 int coll_attn_prompt(int nranks, const void *const *q, const void *const *k,
                      const void *const *v, void *const *o, float *const *lse,
@@ -741,6 +741,9 @@ int coll_kv_compact(int32_t *table, int32_t *ref, int table_rows, int max_pages,
  * (for instance the K and V pools of each rank).  Pairs with an index outside
  * [0, num_pages) are skipped; a page must not be both a source and a
  * destination, nor a destination twice (the lists above never do that).
+ * COLL_ERR_UNSUPPORTED if npools * layers * max_moves copies of a page, in
+ * pieces of 16 KiB (of 1024 smaller units where page_bytes or a pool is not a
+ * multiple of 16), are more than about 2^31.
  */
 int coll_kv_copy_pages(int npools, void *const *pools, size_t layers, size_t num_pages,
                        size_t page_bytes, const int32_t *moves, int max_moves,
