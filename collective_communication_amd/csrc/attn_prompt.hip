@@ -465,7 +465,7 @@ template <int DT, int D>
 int go(const Launch &L, int R, PromptArgs &A, int64_t q_rows) {
   // 8 waves share a staged tile among 256 rows when that gives every compute
   // unit two workgroups' work; otherwise 4 waves and 128 rows, two workgroups
-  // at a time on a compute unit (7476 packed tokens x 32 heads x 128: 136
+  // at a time on a compute unit (6876 packed tokens x 32 heads x 128: 136
   // against 141 us; 4 x 512 tokens: 38 against 28).  Heads of 64 leave room for
   // three workgroups of 4 waves (8192 x 32 heads x 64: 337 against 346 us), heads
   // beyond 128 for one.

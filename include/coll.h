@@ -566,7 +566,8 @@ int coll_moe_combine_recv(int nranks, const void *const *recvbufs, const int32_t
  * coll_lse_merge and coll_seq_heads_reshard: they make the partial outputs and
  * log-sum-exps that the merge joins, over the heads that the re-shard brings
  * together.  As everywhere, one call serves R ranks (tensor parallel: each
- * with its heads; context parallel: each with its part of the keys).
+ * with its heads; context parallel: each with its part of the keys).  The merge
+ * takes bf16 as it is; fp16 partials are widened to fp32 for it.
  *
  * Shared by both attention calls:
  *  - dtype COLL_BF16 or COLL_FP16; head_dim 64, 96, 128, 192 or 256; others
