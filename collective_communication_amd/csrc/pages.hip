@@ -26,14 +26,22 @@ struct PageState {
   FastDiv by_page;
 };
 
-// Inclusive prefix sum over the workgroup's lanes; *total: the whole sum.
+// a + b of numbers from 0 to INT32_MAX, at most INT32_MAX: 1024 entries may ask
+// for more pages together than 32 bits hold.
+__device__ __forceinline__ int add_sat(int a, int b) {
+  const uint32_t s = (uint32_t)a + (uint32_t)b;
+  return (int)(s < 0x7FFFFFFFu ? s : 0x7FFFFFFFu);
+}
+
+// Inclusive prefix sum over the workgroup's lanes, of numbers from 0 on; *total:
+// the whole sum.  Sums stay at INT32_MAX (more than there can be pages).
 __device__ __forceinline__ int scan_block(int x, int *s_wave, int *total) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   int upto = x;
 #pragma unroll
   for (int d = 1; d < 64; d <<= 1) {
     const int y = __shfl_up(upto, d, 64);
-    if (lane >= d) upto += y;
+    if (lane >= d) upto = add_sat(upto, y);
   }
   __syncthreads();
   if (lane == 63) s_wave[wave] = upto;
@@ -42,11 +50,11 @@ __device__ __forceinline__ int scan_block(int x, int *s_wave, int *total) {
 #pragma unroll
   for (int w = 0; w < kOneWaves; w++) {
     const int y = s_wave[w];
-    before += w < wave ? y : 0;
-    all += y;
+    before = add_sat(before, w < wave ? y : 0);
+    all = add_sat(all, y);
   }
   *total = all;
-  return before + upto;
+  return add_sat(before, upto);
 }
 
 __device__ __forceinline__ int pages_of(const PageState &S, int tokens) {

@@ -288,6 +288,22 @@ def state_case(name, S, width, P, N, lens, steps, seed=1):
         same(rf, want.ref.astype(np.int32), f"{name}: ref after {op}")
 
 
+def far_case():
+    """Entries that together ask for more than 2^31 pages: the rows of a table of
+    2^30 columns, of which only the first entry's pages are ever written."""
+    case("pages", "more than 2^31 asked for")
+    S, width, N = 4, 1 << 30, 8
+    t, ln, rf = H.copy(np.full(3, -1, np.int32)), H.copy(np.zeros(S, np.int32)), H.copy(np.zeros(N, np.int32))
+    seqs, add, status = H.copy(np.arange(4, dtype=np.int32)), H.copy(np.array([3] + [1 << 30] * 3, np.int32)), \
+        H.poison((4,), np.int32)
+    ok(cases.L.coll_kv_extend(ptr(t), ptr(ln), ptr(rf), S, width, N, 1, ptr(seqs), ptr(add), 4, ptr(status), None),
+       "extend")
+    same(status, np.array([0, -2, -2, -2], np.int32), "status")
+    same(t, np.arange(3, dtype=np.int32), "pages")
+    same(ln, np.array([3, 0, 0, 0], np.int32), "lens")
+    same(rf, np.array([1] * 3 + [0] * 5, np.int32), "ref")
+
+
 def copy_case(name, pools, layers, N, page_bytes, moves, count=None, seed=1):
     case("copy_pages", name, pools, layers, N, page_bytes)
     g = np.random.default_rng(seed)
@@ -370,6 +386,7 @@ def fam_pages():
                 ("compact",)])
     state_case("rows of a wide table", 60, 700, 4, 700, [30, 2500],
                [("fork", [0, 1, 0] * 10, list(range(5, 35))), ("compact",), ("free", [1, 6])])
+    far_case()
     state_case("nothing free", 3, 4, 2, 4, [8], [("extend", [1], [1]), ("compact",), ("fork", [0], [2])])
     state_case("nothing used", 3, 4, 2, 9, [], [("compact",), ("free", [0, 1])])
     copy_case("one", 1, 1, 4, 64, [(0, 2)])
