@@ -473,7 +473,7 @@ int go(const Launch &L, int R, PromptArgs &A, int64_t q_rows) {
   const bool wide = (D == 96 || D == 128) && tiles8 * A.heads * R >= 2ull * L.num_cus;
   const uint64_t tiles = wide ? tiles8 : (uint64_t)(q_rows + 127) / 128 + A.nseq;
   const uint64_t groups = tiles * A.heads * R;
-  if (groups > 0x7FFFFFFFull) return COLL_ERR_UNSUPPORTED;
+  if (groups * (wide || D > 128 ? 512 : 256) > kMaxThreads) return COLL_ERR_UNSUPPORTED;
   A.tiles = (uint32_t)tiles;
   A.by_tiles = make_fastdiv(A.tiles);
   // D = 96 and 128: both forms; 64: 4 waves; 192 and 256: 8 waves, two to a row

@@ -17,6 +17,7 @@
 namespace coll {
 
 constexpr int kBlock = 256;   // threads per workgroup: 4 wave64s
+constexpr uint64_t kMaxThreads = 0xFFFFFFFFull;   // of a launch: the runtime counts them in 32 bits
 
 struct RankPtrs {
   const void *in[COLL_MAX_RANKS];

@@ -517,12 +517,12 @@ int launch_kv_free(const Launch &L, int32_t *table, int32_t *lens, int32_t *ref,
 int launch_kv_compact(const Launch &L, int32_t *table, int32_t *ref, int rows, int width,
                       int num_pages, int32_t *moves, int max_moves, int32_t *count, int32_t *map) {
   const PageState S = state(table, nullptr, ref, rows, width, num_pages, 1);
+  if ((uint64_t)rows * (uint64_t)width > kMaxThreads - kBlock) return COLL_ERR_UNSUPPORTED;
   hipLaunchKernelGGL(compact_plan, dim3(1), dim3(kOne), 0, L.stream, S, map, moves, max_moves,
                      count);
   const int64_t entries = (int64_t)rows * width;
   if (entries > 0) {
     const int64_t groups = (entries + kBlock - 1) / kBlock;
-    if (groups > 0x7FFFFFFF) return COLL_ERR_UNSUPPORTED;
     hipLaunchKernelGGL(compact_table, dim3((unsigned)groups), dim3(kBlock), 0, L.stream, S,
                        (const int32_t *)map, entries);
   }
@@ -568,7 +568,7 @@ int launch_kv_write(const Launch &L, int R, const PtrTable &k, const PtrTable &v
   A.row_units = A.head_units * (uint32_t)kv_heads;
   A.by_page = make_fastdiv((uint32_t)page_size);
   A.by_head = make_fastdiv(A.head_units);
-  if (tokens * R >= (1ll << 31)) return COLL_ERR_UNSUPPORTED;
+  if ((uint64_t)tokens * R * 64 > kMaxThreads - kBlock) return COLL_ERR_UNSUPPORTED;
   A.by_tokens = make_fastdiv((uint32_t)tokens);
   const uint32_t waves = (uint32_t)(tokens * R), per = kBlock / 64;
   hipLaunchKernelGGL(write_rows, dim3((waves + per - 1) / per), dim3(kBlock), 0, L.stream, A, waves);

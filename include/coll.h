@@ -607,7 +607,9 @@ int coll_moe_combine_recv(int nranks, const void *const *recvbufs, const int32_t
  * query rows do not all lie in [0, q_rows) is not computed; one whose key
  * rows do not all lie in [0, k_rows) has no keys.
  * The launch has a workgroup for each 256 (or 128) query rows and one more per
- * sequence, for each head; q_rows and k_rows are at most 2^31 - 1024.
+ * sequence, for each head of each rank: COLL_ERR_UNSUPPORTED if that is more
+ * than 2^32 - 1 threads (of 512 or 256 a workgroup).  q_rows and k_rows are at
+ * most 2^31 - 1024.
  */
 int coll_attn_prompt(int nranks, const void *const *q, const void *const *k,
                      const void *const *v, void *const *o, float *const *lse,
@@ -663,6 +665,7 @@ int coll_attn_decode(int nranks, const void *const *q, const void *const *k_pool
  * and seqs as in coll_attn_decode; any 16-bit dtype, head_dim a multiple of 8
  * up to 1024.  Rows of no sequence, and rows whose position or page does not
  * exist, are not written.  Two batch entries must not name one sequence.
+ * COLL_ERR_UNSUPPORTED for about 2^26 tokens (over all ranks) or more.
  */
 int coll_kv_write(int nranks, const void *const *k, const void *const *v, void *const *k_pools,
                   void *const *v_pools, const int32_t *const *tables, const int32_t *const *lens,
@@ -729,6 +732,7 @@ int coll_kv_free(int32_t *table, int32_t *lens, int32_t *ref, int table_rows, in
  * the rest -1 (DEVICE int32 [max_moves][2], max_moves >= num_pages / 2).  Pass
  * them to coll_kv_copy_pages for every pool before the pages are read.
  *   workspace: DEVICE, 256-byte aligned, coll_kv_compact_workspace_bytes bytes.
+ * COLL_ERR_UNSUPPORTED for a table of about 2^32 entries or more.
  */
 size_t coll_kv_compact_workspace_bytes(int num_pages);
 int coll_kv_compact(int32_t *table, int32_t *ref, int table_rows, int max_pages, int num_pages,

@@ -49,6 +49,8 @@ def prompt(L, **kw):
     (dict(o=NULL), INVALID), (dict(qs=NULL), INVALID), (dict(ks=t(0x10000, 0)), INVALID),
     (dict(diag=t(0x10000, 0)), INVALID), (dict(q=t(0x10008, 0x20000)), INVALID), (dict(k=t(0x10000, 0x20002)), INVALID),
     (dict(o=t(0x10000, 0x20004)), INVALID), (dict(nseq=0), 0), (dict(q_rows=0), 0),
+    (dict(nseq=1 << 22), UNSUPPORTED), (dict(nseq=1 << 22, D=256, q_stride=1024, o_stride=1024, k_stride=512,
+                                             v_stride=512), UNSUPPORTED),
 ])
 def test_prompt(L, kw, want):
     assert prompt(L, **kw) == want
@@ -105,7 +107,7 @@ def write(L, **kw):
     (dict(ps=2049), INVALID), (dict(P=0), INVALID), (dict(k=NULL), INVALID), (dict(vp=t(0x10000, 0)), INVALID),
     (dict(tab=NULL), INVALID), (dict(lens=NULL), INVALID), (dict(starts=NULL), INVALID),
     (dict(seqs=t(0, 0x10000)), INVALID), (dict(kp=t(0x10008, 0x20000)), INVALID), (dict(width=1 << 28), UNSUPPORTED),
-    (dict(tokens=1 << 31), UNSUPPORTED), (dict(tokens=0), 0), (dict(batch=0), 0), (dict(rows=0), 0), (dict(N=0), 0),
+    (dict(tokens=1 << 31), UNSUPPORTED), (dict(tokens=1 << 26), UNSUPPORTED), (dict(tokens=0), 0), (dict(batch=0), 0), (dict(rows=0), 0), (dict(N=0), 0),
 ])
 def test_write(L, kw, want):
     assert write(L, **kw) == want
@@ -143,6 +145,7 @@ def test_compact_and_copy(L):
     for kw in (dict(table=NULL), dict(ref=NULL), dict(rows=-1), dict(width=-1), dict(N=-1), dict(moves=NULL),
                dict(most=49), dict(count=NULL), dict(ws=NULL), dict(ws=0x10010), dict(ws_bytes=511)):
         assert L.coll_kv_compact(*dict(good, **kw).values(), NULL) == INVALID, kw
+    assert L.coll_kv_compact(*dict(good, rows=1 << 16, width=1 << 16).values(), NULL) == UNSUPPORTED
     good = dict(n=2, pools=P2, layers=3, N=100, page=4096, moves=0x3000, most=50, count=NULL)
     for kw in (dict(n=0), dict(n=17), dict(pools=NULL), dict(pools=t(0x1000, 0)), dict(moves=NULL), dict(most=-1),
                dict(layers=1 << 60), dict(page=1 << 60)):
