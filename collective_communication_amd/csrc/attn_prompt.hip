@@ -356,28 +356,23 @@ __global__ __launch_bounds__(NW * 64, D == 64 ? 3 : 2) void prompt_tiles(PromptA
     // the last
     const bool more_k = kt + 2 < ntiles, more_v = kt + 1 < ntiles;
     if (more_k) load(kp, A.k_stride, kt + 2);
-    if (busy) {
-      raise(s);
-      f32x16 nx[KT];
+    if (busy) raise(s);
 #pragma unroll
-      for (int x = 0; x < KT; x++) {
-        if (x == KT - 1) {
-          if (more_k) store_k(kt + 2);
-          if (more_v) load(vp, A.v_stride, kt + 1);
-        }
-        u32x4 p[2];
-        weights(s[x], p);
-        nx[x] = scores(kt + 1, x);                    // of an old tile after the last one: not used
-#pragma unroll
-        for (int y = 0; y < 2; y++)
-#pragma unroll
-          for (int d = 0; d < DV; d++) acc[d] = mma32<DT>(v_frag(kt, d, 2 * x + y), p[y], acc[d]);
+    for (int x = 0; x < KT; x++) {
+      // (outside of any branch on busy: a wait for a load that only one side has
+      // in flight would be paid on both)
+      if (x == KT - 1) {
+        if (more_k) store_k(kt + 2);
+        if (more_v) load(vp, A.v_stride, kt + 1);
       }
+      if (!busy) continue;
+      u32x4 p[2];
+      weights(s[x], p);
+      s[x] = scores(kt + 1, x);                       // of an old tile after the last one: not used
 #pragma unroll
-      for (int x = 0; x < KT; x++) s[x] = nx[x];
-    } else {
-      if (more_k) store_k(kt + 2);
-      if (more_v) load(vp, A.v_stride, kt + 1);
+      for (int y = 0; y < 2; y++)
+#pragma unroll
+        for (int d = 0; d < DV; d++) acc[d] = mma32<DT>(v_frag(kt, d, 2 * x + y), p[y], acc[d]);
     }
     if (more_v) store_v(kt + 1);
     __syncthreads();
