@@ -733,6 +733,7 @@ int coll_attn_prompt(int R, const void *const *q, const void *const *k, const vo
   if (!rows_ok(q_rows, q_stride, qw) || !rows_ok(q_rows, o_stride, qw) ||
       !rows_ok(k_rows, k_stride, kw) || !rows_ok(k_rows, v_stride, kw))
     return COLL_ERR_INVALID_ARG;
+  if (k_stride > kPromptMaxStride || v_stride > kPromptMaxStride) return COLL_ERR_UNSUPPORTED;
   PtrTable qt{}, kt{}, vt{}, qs{}, ks{}, dg{};
   MutPtrTable ot{}, lt{};
   if (!fill_in(R, q, qt.p) || !fill_out(R, o, ot.p) ||

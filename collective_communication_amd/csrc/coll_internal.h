@@ -584,6 +584,7 @@ int launch_kv_write(const Launch &L, int R, const PtrTable &k, const PtrTable &v
                     int64_t page_stride, int64_t tok_stride, int64_t head_stride);
 // entries of one bookkeeping call: one lane each
 constexpr int kKvMaxEntries = COLL_KV_MAX_ENTRIES;
+constexpr int64_t kPromptMaxStride = 1 << 25;   // of keys: the places in a tile of 64 fit 32 bits of bytes
 int launch_kv_extend(const Launch &L, int32_t *table, int32_t *lens, int32_t *ref, int rows,
                      int width, int num_pages, int page_size, const int32_t *seqs,
                      const int32_t *add, int n, int32_t *status);

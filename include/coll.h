@@ -602,7 +602,8 @@ int coll_moe_combine_recv(int nranks, const void *const *recvbufs, const int32_t
  *   o_i = sum_j p_ij v_j / sum_j p_ij,  p_ij = exp(scale q_i . k_j - max),
  *   lse_i = log sum_j exp(scale q_i . k_j), over the keys i sees.
  *   q[r], o[r]: q_rows tokens of heads * head_dim elements, q_stride and
- *   o_stride elements apart; k[r], v[r]: k_rows tokens of kv_heads * head_dim.
+ *   o_stride elements apart; k[r], v[r]: k_rows tokens of kv_heads * head_dim,
+ *   k_stride and v_stride apart (COLL_ERR_UNSUPPORTED over 2^25).
  * Rows that belong to no sequence are left as they are.  A sequence whose
  * query rows do not all lie in [0, q_rows) is not computed; one whose key
  * rows do not all lie in [0, k_rows) has no keys.

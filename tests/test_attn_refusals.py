@@ -49,6 +49,7 @@ def prompt(L, **kw):
     (dict(o=NULL), INVALID), (dict(qs=NULL), INVALID), (dict(ks=t(0x10000, 0)), INVALID),
     (dict(diag=t(0x10000, 0)), INVALID), (dict(q=t(0x10008, 0x20000)), INVALID), (dict(k=t(0x10000, 0x20002)), INVALID),
     (dict(o=t(0x10000, 0x20004)), INVALID), (dict(nseq=0), 0), (dict(q_rows=0), 0),
+    (dict(k_stride=(1 << 25) + 8), UNSUPPORTED), (dict(v_stride=1 << 26), UNSUPPORTED),
     (dict(nseq=1 << 22), UNSUPPORTED), (dict(nseq=1 << 22, D=256, q_stride=1024, o_stride=1024, k_stride=512,
                                              v_stride=512), UNSUPPORTED),
 ])
