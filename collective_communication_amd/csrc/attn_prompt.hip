@@ -207,7 +207,11 @@ __global__ __launch_bounds__(NW * 64, D == 64 ? 3 : 2) void prompt_tiles(PromptA
     for (int s = 0; s < DK; s++) q[s] = ld<u32x4>(qp, 2 * s + g) ^ sign;
   }
 
-  // a thread's chunks of a tile: key kr0[i] of the tile, 16 bytes at chunk c
+  // a thread's chunks of a tile: 16 bytes at chunk_of of key key_of (whole steps
+  // from one to the next where the threads take whole keys: one address)
+  constexpr bool kSteps = NT % CH == 0;
+  auto key_of = [](int t, int i) -> int { return kSteps ? t / CH + i * (NT / CH) : (t + i * NT) / CH; };
+  auto chunk_of = [](int t, int i) -> int { return kSteps ? t % CH : (t + i * NT) % CH; };
   u32x4 held[NCH];
   const char *kp = reinterpret_cast<const char *>(A.k.p[r]) + (t.k0 * A.k_stride + (int64_t)kvh * D) * 2;
   const char *vp = reinterpret_cast<const char *>(A.v.p[r]) + (t.k0 * A.v_stride + (int64_t)kvh * D) * 2;
@@ -215,10 +219,12 @@ __global__ __launch_bounds__(NW * 64, D == 64 ? 3 : 2) void prompt_tiles(PromptA
   // the last: its score is masked, and a value that is not finite marks the
   // tile in any case.  So no load needs a branch.
   auto places = [&](uint32_t (&at)[NCH], int64_t stride, int rows) {
+    int me = tid;
+    COLL_FRESH(me);
 #pragma unroll
     for (int i = 0; i < NCH; i++) {
-      const int x = tid + i * NT, kr = x / CH, c = x - kr * CH, last = (rows < BN ? rows : BN) - 1;
-      at[i] = (uint32_t)(kr < last ? kr : last) * (uint32_t)(2 * stride) + 16 * c;
+      const int kr = key_of(me, i), last = (rows < BN ? rows : BN) - 1;
+      at[i] = (uint32_t)(kr < last ? kr : last) * (uint32_t)(2 * stride) + 16 * chunk_of(me, i);
     }
   };
   uint32_t k_at[NCH], v_at[NCH];
@@ -231,10 +237,9 @@ __global__ __launch_bounds__(NW * 64, D == 64 ? 3 : 2) void prompt_tiles(PromptA
   };
   auto store = [&](uint16_t *tile, int row) {
 #pragma unroll
-    for (int i = 0; i < NCH; i++) {
-      const int x = tid + i * NT, kr = x / CH, c = x - kr * CH;
-      if (kWhole || x < BN * CH) *reinterpret_cast<u32x4 *>(tile + kr * row + 8 * c) = held[i];
-    }
+    for (int i = 0; i < NCH; i++)
+      if (kWhole || key_of(tid, i) < BN)
+        *reinterpret_cast<u32x4 *>(tile + key_of(tid, i) * row + 8 * chunk_of(tid, i)) = held[i];
   };
   auto store_k = [&](int kt) { store(s_t.k[kt & 1], TL::kRowK); };
   auto store_v = [&](int kt) {
@@ -384,18 +389,20 @@ __global__ __launch_bounds__(NW * 64, D == 64 ? 3 : 2) void prompt_tiles(PromptA
     __syncthreads();
   }
   for (; kt < ntiles; kt++) {                         // tiles on the diagonal and the last one
-    if (kt + 2 < ntiles) {
-      load(kp, A.k_stride, k_at, kt + 2);
-      store_k(kt + 2);
-    }
-    if (kt + 1 < ntiles) load(vp, A.v_stride, v_at, kt + 1);
-    if (kt * BN < n_wave) {
+    const bool more_k = kt + 2 < ntiles, more_v = kt + 1 < ntiles, sees = kt * BN < n_wave;
+    if (more_k) load(kp, A.k_stride, k_at, kt + 2);
+    if (sees) {
+      const int left = lim - kt * BN - 4 * g;
 #pragma unroll
       for (int x = 0; x < KT; x++)
 #pragma unroll
         for (int e = 0; e < 16; e++)
-          s[x][e] = kt * BN + 32 * x + (e & 3) + 8 * (e >> 2) + 4 * g < lim ? s[x][e] : -__builtin_inff();
+          s[x][e] = 32 * x + (e & 3) + 8 * (e >> 2) < left ? s[x][e] : -__builtin_inff();
       raise(s);
+    }
+    if (more_k) store_k(kt + 2);
+    if (more_v) load(vp, A.v_stride, v_at, kt + 1);
+    if (sees) {
       const bool bad = s_bad[kt & 1] == kt + 1;
 #pragma unroll
       for (int x = 0; x < KT; x++) {
@@ -411,6 +418,8 @@ __global__ __launch_bounds__(NW * 64, D == 64 ? 3 : 2) void prompt_tiles(PromptA
           continue;
         }
         // key by key, each added only where it is visible
+        int half = g;
+        COLL_FRESH(half);
         for (int j = 0; j < 32; j++) {
           const int jj = j & 15;
           // the key's place in the operands: half of the wave and element
@@ -418,7 +427,7 @@ __global__ __launch_bounds__(NW * 64, D == 64 ? 3 : 2) void prompt_tiles(PromptA
           u32x4 keep;
 #pragma unroll
           for (int w = 0; w < 4; w++)
-            keep[w] = (g == gj && ej >> 1 == w) ? (ej & 1 ? 0xFFFF0000u : 0xFFFFu) : 0u;
+            keep[w] = (half == gj && ej >> 1 == w) ? (ej & 1 ? 0xFFFF0000u : 0xFFFFu) : 0u;
           const u32x4 pj = (j < 16 ? p[0] : p[1]) & keep;
           const bool vis = key0 + j < lim;
 #pragma unroll
@@ -436,7 +445,7 @@ __global__ __launch_bounds__(NW * 64, D == 64 ? 3 : 2) void prompt_tiles(PromptA
       for (int x = 0; x < KT; x++)
         if ((kt + 1) * BN + 32 * x < n_wave) s[x] = scores(kt + 1, x);
     }
-    if (kt + 1 < ntiles) store_v(kt + 1);
+    if (more_v) store_v(kt + 1);
     __syncthreads();
   }
   float l = l0 + l1;
@@ -464,14 +473,17 @@ __global__ __launch_bounds__(NW * 64, D == 64 ? 3 : 2) void prompt_tiles(PromptA
 
 template <int DT, int D>
 int go(const Launch &L, int R, PromptArgs &A, int64_t q_rows) {
-  // 8 waves share a staged tile among 256 rows when that gives every compute
-  // unit two workgroups' work; otherwise 4 waves and 128 rows, two workgroups
-  // at a time on a compute unit (6876 packed tokens x 32 heads x 128: 136
-  // against 141 us; 4 x 512 tokens: 38 against 28).  Heads of 64 leave room for
-  // three workgroups of 4 waves (8192 x 32 heads x 64: 337 against 346 us), heads
-  // beyond 128 for one.
+  // 8 waves share a staged tile among 256 rows when the sequences are long (4096
+  // keys and more, on average) and give every compute unit two workgroups' work;
+  // otherwise 4 waves and 128 rows, two workgroups at a time on a compute unit,
+  // so that one computes while the other begins, ends or waits at the diagonal
+  // (32 heads x 128: 8192 tokens 555 against 568 us; 8 x 2048: 375 against 363; 8 x
+  // 1024: 132 against 114; 32 x 256: 95 against 71; 4096 x 32 heads x 96: 130
+  // against 133).  Heads of 64 leave room for three workgroups of 4 waves (8192 x
+  // 32 heads x 64: 337 against 346 us), heads beyond 128 for one.
   const uint64_t tiles8 = (uint64_t)(q_rows + 255) / 256 + A.nseq;
-  const bool wide = (D == 96 || D == 128) && tiles8 * A.heads * R >= 2ull * L.num_cus;
+  const bool wide = (D == 96 || D == 128) && A.k_rows / A.nseq >= 4096 &&
+                    tiles8 * A.heads * R >= 2ull * L.num_cus;
   const uint64_t tiles = wide ? tiles8 : (uint64_t)(q_rows + 127) / 128 + A.nseq;
   const uint64_t groups = tiles * A.heads * R;
   if (groups * (wide || D > 128 ? 512 : 256) > kMaxThreads) return COLL_ERR_UNSUPPORTED;

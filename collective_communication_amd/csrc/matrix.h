@@ -76,6 +76,12 @@ __device__ __forceinline__ float max_halves(float x) {
   asm volatile("" ::"s"(a), "s"(b), "s"(c), "s"(d), "s"(e), "s"(f), "s"(g), "s"(h))
 #endif
 
+// x as if computed anew here: what is rarely needed is then not computed ahead
+// of a loop and kept (or spilled) through it.  Emits no instruction.
+#ifndef COLL_FRESH
+#define COLL_FRESH(x) asm volatile("" : "+v"(x))
+#endif
+
 // Two fp32 -> a pair of the 16-bit type, round to nearest even.
 template <int DT>
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {

@@ -116,6 +116,13 @@ def fam_prompt():
     prompt_case("infinities and NaN behind the diagonal", 1, 2, 1, 64, [100], [100], plant=bad_v)
     prompt_case("... and 8 waves", 1, 8, 1, 128, [260], [260], plant=bad_v)
 
+    # sequences of 4096 keys and more take 256 rows at a time, of 96 and 128 elements
+    def far(q, k, v):
+        v[4100], v[4120, :7], k[4130] = 0x7E00, 0xFF80, 0x7FC1
+    prompt_case("eight waves, long", 1, 4, 2, 96, [262], [4131], plant=far, seed=5)
+    prompt_case("eight waves, long, partly unseen", 2, 4, 4, 128, [3, 35], [4110, 4161], dtype="fp16", seed=6,
+                diag=[[4000, 4140], [-1, 10000]])
+
     def bad_tail(q, k, v):
         v[-3:], k[-3:] = 0x7FC1, 0x7F80
     prompt_case("NaN behind the last sequence", 1, 2, 1, 128, [45, 37], [45, 37], plant=bad_tail, tail=3)

@@ -34,6 +34,7 @@
 #define COLL_KEEP(x) ((void)0)
 #define COLL_SCALAR(x) ((void)0)
 #define COLL_FETCH(...) ((void)0)
+#define COLL_FRESH(x) ((void)0)
 // ld_scalar: the GPU reads through the scalar cache, which needs the address
 // to be the same in every lane; here it is a plain load, after checking that
 // every active lane asks for the same address (defined below emu_uniform_at)

@@ -102,6 +102,17 @@ def test_prompt_long():
     run_prompt("long", 1, 1, 1, 128, [4100], [4100], seed=10)
 
 
+@pytest.mark.parametrize("D,dtype", [(96, "fp16"), (96, "bf16"), (128, "fp16"), (128, "bf16")])
+def test_prompt_of_256_rows_at_a_time(D, dtype):
+    """Long sequences that fill the card, of 96 and 128 elements; unseen keys that are not finite."""
+    def far(q, k, v):
+        v[4095], v[4200, :, :7], k[4150] = 0x7FC1, 0xFF80, 0x7FC1
+    run_prompt("256 rows", 2, 64, 4, D, [260, 3], [4205, 4001], dtype, seed=D + 30, plant=far)
+    run_prompt("256 rows, all keys", 1, 128, 16, D, [257, 2], [4099, 4100], dtype, causal=False, seed=D + 31)
+    run_prompt("256 rows, diagonals", 2, 64, 8, D, [250, 7], [4105, 4100], dtype, seed=D + 32,
+               diag=[[3900, -3], [-100, 4096]])
+
+
 def test_prompt_diagonals():
     lens = [150, 97]
     diag = [[(5 - r) * n for n in lens] for r in range(8)]
