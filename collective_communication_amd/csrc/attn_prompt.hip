@@ -175,6 +175,10 @@ __global__ __launch_bounds__(NW * 64, D == 64 ? 3 : 2) void prompt_tiles(PromptA
   if (H % 8 == 0) h = (h & 7) * (H / 8) + (h >> 3);
   const int r = (int)fdiv(th, A.by_tiles);
   const uint32_t tile = A.tiles - 1 - (th - (uint32_t)r * A.tiles);
+  // (8192 x 32 heads x 128: 553 -> 545 us)
+  COLL_FETCH(A.q_starts.p[r], A.k_starts.p[r], A.diag.p[r], A.q.p[r], A.k.p[r], A.v.p[r], A.nseq, A.q_rows);
+  COLL_FETCH(A.k_rows, A.q_stride, A.k_stride, A.v_stride, A.by_group.m, A.c, A.negate, A.causal);
+  COLL_FETCH(A.o.p[r], A.lse.p[r], A.o_stride, A.heads, A.kv_heads, A.tiles, A.by_heads.m, A.by_tiles.m);
   const TileAt t = find_tile<BQ>(A, r, A.tiles - 1 - tile);
   if (!t.any) return;
   const int kvh = (int)fdiv(h, A.by_group);
