@@ -51,26 +51,15 @@ __device__ __forceinline__ int32_t span(int64_t a, int64_t b, int64_t n) {
   return (a < 0 || b <= a || b > n) ? 0 : (int32_t)(b - a);
 }
 
-// Largest of the lanes' values (below 2^12), a bit at a time.
-__device__ __forceinline__ uint32_t wave_max(uint32_t x) {
-  uint64_t in = ~0ull;
-  uint32_t top = 0;
-#pragma unroll
-  for (int b = 11; b >= 0; b--) {
-    const uint64_t has = __ballot((x >> b) & 1) & in;
-    if (has) {
-      in = has;
-      top |= 1u << b;
-    }
-  }
-  return top;
-}
-
 // The sequence that holds tile slot `slot` of rank r, scanned by every wave, 64
 // sequences at a time.  Causal tiles get longer towards a sequence's end, and
-// the last workgroups to start should be short: up to 64 sequences of up to 64
-// tiles are taken level by level, every sequence's 64th tile first (packed
-// prompts of 1 to 2048 tokens: 148 -> 137 us); others from the last tile down.
+// the last workgroups to start should be short: 2 to 16 sequences of up to 64
+// tiles are taken level by level, every sequence's 64th tile first (8 packed
+// prompts of 1 to 2048 tokens: 136 -> 125 us, 4 of 512: 28 -> 24); others from
+// the last tile down (a look-up for each sequence, it costs more than it gives
+// for 32 sequences of 512 or 256 tokens: 173 and 75 us against 160 and 65).
+// Sums over the lanes go by lane reads and ballots: a shuffle is a trip to LDS,
+// and this is before a workgroup's first load.
 template <int BQ>
 __device__ __forceinline__ TileAt find_tile(const PromptArgs &A, int r, uint32_t slot) {
   const int32_t *qs = reinterpret_cast<const int32_t *>(A.q_starts.p[r]);
@@ -78,6 +67,7 @@ __device__ __forceinline__ TileAt find_tile(const PromptArgs &A, int r, uint32_t
   const int32_t *dg = reinterpret_cast<const int32_t *>(A.diag.p[r]);
   const int lane = threadIdx.x & 63;
   const uint32_t tile = A.tiles - 1 - slot;
+  const uint64_t to_me = (2ull << lane) - 1;          // the lanes up to this one
   TileAt t{};
   uint32_t before = 0;
   for (int base = 0; base < A.nseq; base += 64) {
@@ -94,27 +84,24 @@ __device__ __forceinline__ TileAt find_tile(const PromptArgs &A, int r, uint32_t
     const uint32_t mine = ((uint32_t)nq + BQ - 1) / BQ;
     int l = -1;
     uint32_t index = 0;
-    const uint32_t most = A.nseq <= 64 && !__ballot(mine > 64) ? wave_max(mine) : 0;
-    if (most > 0) {
-      uint32_t rest = slot;
-      for (int level = (int)most - 1; level >= 0; level--) {
-        uint64_t in = __ballot(mine > (uint32_t)level);
-        const uint32_t n = (uint32_t)__popcll(in);
-        if (rest < n) {
-          for (; rest > 0; rest--) in &= in - 1;
-          l = __builtin_ctzll(in);
-          index = (uint32_t)level;
-          break;
-        }
-        rest -= n;
+    if (A.nseq > 1 && A.nseq <= 16 && !__ballot(mine > 64)) {
+      uint32_t high = 0;                              // tiles of level `lane` and above
+      for (int x = 0; x < A.nseq; x++) {
+        const int m = __builtin_amdgcn_readlane((int)mine, x);
+        high += m > lane ? m - lane : 0;
+      }
+      const uint64_t above = __ballot(high > slot);   // the levels up to the slot's
+      if (above) {
+        const int level = 63 - __builtin_clzll(above);
+        const uint32_t rest = slot - (level < 63 ? (uint32_t)__builtin_amdgcn_readlane((int)high, level + 1) : 0);
+        const uint64_t in = __ballot(mine > (uint32_t)level);
+        l = __builtin_ctzll(__ballot(mine > (uint32_t)level && (uint32_t)__popcll(in & (to_me >> 1)) == rest));
+        index = (uint32_t)level;
       }
     } else {
-      uint32_t upto = mine;
-#pragma unroll
-      for (int x = 1; x < 64; x <<= 1) {
-        const uint32_t y = __shfl_up(upto, x, 64);
-        if (lane >= x) upto += y;
-      }
+      uint32_t upto = 0;
+      for (int x = 0; __ballot(mine >> x != 0); x++)
+        upto += (uint32_t)__popcll(__ballot((mine >> x) & 1) & to_me) << x;
       const uint64_t hit = __ballot(before + upto > tile);
       if (hit) {
         l = __builtin_ctzll(hit);
