@@ -18,6 +18,10 @@
 // is read: the transposing LDS read takes 4 consecutive keys at a time.
 // K and V tiles are staged through registers into two LDS buffers (one
 // barrier per tile).
+//
+// At 128 elements a head it runs at 1000 to 1060 TFLOP/s (8192 tokens x 32 heads:
+// 545 us causal, 1035 us with all keys), four fifths of what a large library
+// product reaches: matrix pipe 50%, vector pipe 41% and LDS 31% of the cycles.
 #include "matrix.h"
 
 #pragma clang fp contract(off)
@@ -126,7 +130,8 @@ __device__ __forceinline__ TileAt find_tile(const PromptArgs &A, int r, uint32_t
 // Waves that share 32 query rows.  Beyond 128 elements the registers of a wave
 // that holds whole rows would leave a SIMD one wave; two waves then compute the
 // same scores and weights, and each half of the output's columns (4096 causal
-// tokens x 16 heads x 256: 251 us against 390, x 192: 189 against 220).
+// tokens x 16 heads x 256: 251 us against 390, x 192: 189 against 220; by now
+// 212 and 162).
 template <int D>
 constexpr int kSplit = D > 128 ? 2 : 1;
 
